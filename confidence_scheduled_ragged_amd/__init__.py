@@ -63,12 +63,20 @@ def lib() -> ctypes.CDLL:
         L.dspark_workspace_bytes.argtypes = [I, I, I]
         L.dspark_workspace_bytes.restype = S
         L.dspark_workspace_init.argtypes = [P, S, P]
+        L.dspark_append_kv.argtypes = [P, P, P, LL, LL, LL, P, P, I, I, I, P, P, I, I, I, I, I, P,
+                                       P, I, I, I, LL, LL, LL, F, F, P, I, P, P]
+        L.dspark_verify_attention.argtypes = [P, LL, LL, P, P, I, I, I, LL, LL, LL, F, F, P, I, P,
+                                              P, I, I, I, I, I, I, I, F, P, P, S, P]
+        L.dspark_attention_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.dspark_attention_workspace_bytes.restype = S
+        L.dspark_sample_accept.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, P, P, P, P, S, P]
         L.dspark_status_string.argtypes = [I]
         L.dspark_status_string.restype = ctypes.c_char_p
         for f in (L.dspark_confidence, L.dspark_schedule, L.dspark_compact, L.dspark_accept,
                   L.dspark_step, L.dspark_workspace_init, L.dspark_cap_accept,
                   L.dspark_gather_rows, L.dspark_tier_select, L.dspark_cost_cutoff,
-                  L.dspark_step_ex, L.dspark_step_status, L.dspark_step_noalloc):
+                  L.dspark_step_ex, L.dspark_step_status, L.dspark_step_noalloc,
+                  L.dspark_append_kv, L.dspark_verify_attention, L.dspark_sample_accept):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -515,11 +523,179 @@ def dspark_step_status(ws=None, status=None, device=None):
     return status
 
 
+# ------------------------------------------- around the target's verify forward
+
+_CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+
+
+def _paged(k_cache, v_cache, cu_seqlens, ctx_lens, block_table):
+    """Checks the paged cache and the packed batch's lengths; returns B, the
+    cache's type, sizes and strides."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape, [pages, Hkv, page_size, D]")
+    if k_cache.device.type != "cuda" or v_cache.device != k_cache.device:
+        raise ValueError(f"the caches must be on one GPU (got {k_cache.device}, {v_cache.device})")
+    if k_cache.dtype not in _CACHE_TYPES or v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"the caches must be bfloat16 or float8_e4m3fn (got {k_cache.dtype}, "
+                        f"{v_cache.dtype})")
+    strides = k_cache.stride()
+    if v_cache.stride() != strides or strides[3] != 1:
+        raise ValueError("k_cache and v_cache must share strides, with D contiguous")
+    B = cu_seqlens.numel() - 1
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    _need(ctx_lens, "ctx_lens", torch.int32, (B,))
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, pages of a request)")
+    return B, _CACHE_TYPES[k_cache.dtype], k_cache.shape, strides
+
+
+def _packed_heads(t, name, rows, heads, D):
+    """Checks packed [rows, heads, D] bf16 with rows at any stride."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16} (got {t.dtype})")
+    if tuple(t.shape) != (rows, heads, D):
+        raise ValueError(f"{name} must have shape {(rows, heads, D)} (got {tuple(t.shape)})")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have its last axis contiguous")
+    return t
+
+
+def dspark_append_kv(q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cache, v_cache,
+                     interleaved=False, k_scale=1.0, v_scale=1.0, out=None):
+    """Rotates the packed rows' queries and keys by their positions and writes
+    keys and values into the paged cache; returns the rotated queries.
+    q [rows, Hq, D], k and v [rows, Hkv, D] bf16 (views of one projection, with
+    heads side by side), cos and sin [positions, rot / 2] fp32, ctx_lens [B]
+    tokens cached before the call, block_table [B, width] int32, k_cache and
+    v_cache [pages, Hkv, page_size, D] bf16 or float8_e4m3fn."""
+    B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(k_cache, v_cache, cu_seqlens,
+                                                             ctx_lens, block_table)
+    rows, Hq = q.shape[0], q.shape[1]
+    _packed_heads(q, "q", rows, Hq, D)
+    _packed_heads(k, "k", rows, Hkv, D)
+    _packed_heads(v, "v", rows, Hkv, D)
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        if t.stride(1) != D and t.shape[1] > 1:
+            raise ValueError(f"{n} must have its heads side by side")
+    _need(cos, "cos", torch.float32)
+    _need(sin, "sin", torch.float32, cos.shape)
+    if cos.dim() != 2:
+        raise ValueError("cos must have shape (positions, rotated pairs)")
+    dev = q.device
+    out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
+    _need(out, "out", torch.bfloat16, (rows, Hq, D))
+    _ok("dspark_append_kv", lib().dspark_append_kv(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), k.stride(0), v.stride(0),
+        cos.data_ptr(), sin.data_ptr(), cos.shape[0], cos.shape[1], 1 if interleaved else 0,
+        cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, rows, Hq, Hkv, D, k_cache.data_ptr(),
+        v_cache.data_ptr(), kind, pages, page, ps, hs, ss, k_scale, v_scale,
+        block_table.data_ptr(), block_table.shape[1], out.data_ptr(), _stream(dev)))
+    return out
+
+
+def dspark_attention_workspace_bytes(B: int, max_rows: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().dspark_attention_workspace_bytes(B, max_rows, Hq, Hkv, D))
+
+
+_ATTN_WS: Dict[tuple, torch.Tensor] = {}
+
+
+def attention_workspace(B: int, max_rows: int, Hq: int, Hkv: int, D: int, device) -> torch.Tensor:
+    """A zero-initialised workspace of dspark_verify_attention, cached per
+    device. Calls sharing it must not overlap in time."""
+    device = torch.device(device)
+    need = dspark_attention_workspace_bytes(B, max_rows, Hq, Hkv, D)
+    if need == 0:
+        raise ValueError(f"invalid sizes B={B} max_rows={max_rows} Hq={Hq} Hkv={Hkv} D={D}")
+    key = _ws_key(device)
+    ws = _ATTN_WS.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        dspark_workspace_init(ws)
+        _ATTN_WS[key] = ws
+    return ws
+
+
+def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, max_rows,
+                            window=0, scale=None, k_scale=1.0, v_scale=1.0, out=None, ws=None):
+    """Attention of the packed rows q [rows, Hq, D] bf16 over each request's
+    pages, causal at the end of the request: row j of request b stands at
+    position ctx_lens[b] + j, which the cache already holds. max_rows bounds the
+    rows of a request (1 for plain decoding, gamma + 1 for a verify window, any
+    number for a prompt chunk); window > 0 keeps the last `window` positions;
+    scale defaults to D ** -0.5. Returns out [rows, Hq, D] bf16."""
+    B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(k_cache, v_cache, cu_seqlens,
+                                                             ctx_lens, block_table)
+    rows, Hq = q.shape[0], q.shape[1]
+    _packed_heads(q, "q", rows, Hq, D)
+    dev = q.device
+    out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
+    _need(out, "out", torch.bfloat16, (rows, Hq, D))
+    max_rows = min(int(max_rows), rows)
+    if ws is None:
+        ws = attention_workspace(B, max_rows, Hq, Hkv, D, dev)
+    else:
+        _need(ws, "ws", torch.uint8)
+    _ok("dspark_verify_attention", lib().dspark_verify_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), kind,
+        pages, page, ps, hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
+        cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, rows, max_rows, Hq, Hkv, D, int(window),
+        D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(dev)))
+    return out
+
+
+def dspark_sample_accept(logits, packed_src_row, cu_seqlens, tokens, uniforms, temperature=None,
+                         top_k=None, top_p=None, min_p=None, out=None, ws=None):
+    """dspark_accept with the target's tokens drawn: (packed_sample, accepted,
+    bonus). uniforms fp32 [B*(gamma+1)] in [0, 1), one per packed row;
+    temperature (<= 0: greedy), top_p, min_p fp32 [B] and top_k int32 [B] (0:
+    off) per request, None for temperature 1 and no filter. packed_src_row None
+    means `logits` is already packed."""
+    B, g1 = tokens.shape
+    cap = B * g1
+    _need(logits, "logits", torch.bfloat16)
+    V = logits.shape[-1]
+    if logits.numel() != cap * V:
+        raise ValueError("logits must hold B*(gamma+1) rows of V entries")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _need(tokens, "tokens", torch.int32)
+    _need(uniforms, "uniforms", torch.float32, (cap,))
+    if packed_src_row is not None:
+        _need(packed_src_row, "packed_src_row", torch.int32, (cap,))
+    for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")):
+        if t is not None:
+            _need(t, n, torch.float32, (B,))
+    if top_k is not None:
+        _need(top_k, "top_k", torch.int32, (B,))
+    dev = tokens.device
+    out = out or {}
+    smp = out.get("packed_sample")
+    acc = out.get("accepted")
+    bon = out.get("bonus")
+    smp = torch.full((cap,), -1, dtype=torch.int32, device=dev) if smp is None else smp
+    acc = torch.empty(B, dtype=torch.int32, device=dev) if acc is None else acc
+    bon = torch.empty(B, dtype=torch.int32, device=dev) if bon is None else bon
+    _need(smp, "packed_sample", torch.int32, (cap,))
+    _need(acc, "accepted", torch.int32, (B,))
+    _need(bon, "bonus", torch.int32, (B,))
+    ws = workspace(B, g1 - 1, V, dev) if ws is None else _need(ws, "ws", torch.uint8)
+    _ok("dspark_sample_accept", lib().dspark_sample_accept(
+        _ptr(logits), _ptr(packed_src_row), _ptr(cu_seqlens), _ptr(tokens), _ptr(uniforms),
+        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), B, g1 - 1, V, _ptr(smp),
+        _ptr(acc), _ptr(bon), _ptr(ws), ws.numel(), _stream(dev)))
+    return smp, acc, bon
+
+
 __all__ = ["DsparkError", "lib", "LIB_PATH", "dspark_status_string", "dspark_confidence", "dspark_schedule",
            "dspark_compact", "dspark_accept", "dspark_step", "dspark_cap_accept",
            "dspark_gather_rows", "dspark_tier_select", "dspark_cost_cutoff",
            "dspark_step_ex", "dspark_step_status", "dspark_step_noalloc", "BoundStep", "bind_step",
-           "dspark_workspace_bytes",
+           "dspark_append_kv", "dspark_verify_attention", "dspark_sample_accept",
+           "dspark_attention_workspace_bytes", "attention_workspace", "dspark_workspace_bytes",
            "dspark_workspace_init", "workspace", "alloc_step_outputs", "STEP_OUTPUTS",
            "DSPARK_CUT_THRESHOLD", "DSPARK_CUT_BUDGET", "DSPARK_CUT_STATIC",
            "DSPARK_CUT_COMBINED"]

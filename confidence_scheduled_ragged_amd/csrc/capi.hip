@@ -4,7 +4,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "common.hpp"
+#include "forward.hpp"
 
 #define DSPARK_API extern "C" __attribute__((visibility("default")))
 
@@ -409,4 +409,181 @@ DSPARK_API dspark_status dspark_step_noalloc(
                                    ws, s, nullptr, nullptr, 0, 0);
     if (st == DSPARK_OK && status) st = launched(launch_step_status(ws, status, s));
     return st;
+}
+
+namespace {
+
+constexpr int kMaxHeads = 4096;
+
+// The checks that appending to the paged cache and reading it share.
+dspark_status check_paged(const void *k_cache, const void *v_cache, int cache_type, int pages,
+                          int page_size, long long page_stride, long long head_stride,
+                          long long slot_stride, float k_scale, float v_scale, int table_width,
+                          int B, int rows, int Hq, int Hkv, int D, int max_d) {
+    if (B < 1 || rows < 1 || rows > DSPARK_MAX_ROWS || B > DSPARK_MAX_ROWS) return DSPARK_ERR_SHAPE;
+    if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > kMaxHeads) return DSPARK_ERR_SHAPE;
+    if (D < 1 || D > max_d || pages < 1 || page_size < 1 || table_width < 1) return DSPARK_ERR_SHAPE;
+    // positions are 32-bit
+    if ((long long)table_width * page_size > 0x7FFFFFFFll) return DSPARK_ERR_SHAPE;
+    if (cache_type != DSPARK_CACHE_BF16 && cache_type != DSPARK_CACHE_E4M3) return DSPARK_ERR_ARG;
+    if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale <= 0.f || v_scale <= 0.f)
+        return DSPARK_ERR_ARG;
+    if (page_stride < 0 || head_stride < 0 || slot_stride < 0) return DSPARK_ERR_ARG;
+    const size_t item = cache_type == DSPARK_CACHE_E4M3 ? 1 : 2;
+    if (misaligned(k_cache, item) || misaligned(v_cache, item)) return DSPARK_ERR_ALIGN;
+    return DSPARK_OK;
+}
+
+PagedCache paged(const void *k_cache, const void *v_cache, int pages, int page_size,
+                 long long page_stride, long long head_stride, long long slot_stride,
+                 float k_scale, float v_scale, bool scaled, const int32_t *table,
+                 int table_width) {
+    PagedCache c;
+    c.k = const_cast<void *>(k_cache);
+    c.v = const_cast<void *>(v_cache);
+    c.table = table;
+    c.table_width = table_width;
+    c.pages = pages;
+    set_page_size(c, page_size);
+    c.page_stride = page_stride;
+    c.head_stride = head_stride;
+    c.slot_stride = slot_stride;
+    c.k_scale = scaled ? k_scale : 1.f;
+    c.v_scale = scaled ? v_scale : 1.f;
+    return c;
+}
+
+}  // namespace
+
+DSPARK_API dspark_status dspark_append_kv(
+    const dspark_bf16 *q, const dspark_bf16 *k, const dspark_bf16 *v, long long q_stride,
+    long long k_stride, long long v_stride, const float *cos, const float *sin, int positions,
+    int half, int interleaved, const int32_t *cu_seqlens, const int32_t *ctx_lens, int B, int rows,
+    int Hq, int Hkv, int D, void *k_cache, void *v_cache, int cache_type, int pages, int page_size,
+    long long page_stride, long long head_stride, long long slot_stride, float k_scale,
+    float v_scale, const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
+    if (!q || !k || !v || !cu_seqlens || !ctx_lens || !k_cache || !v_cache || !block_table || !q_out)
+        return DSPARK_ERR_NULL;
+    if (half > 0 && (!cos || !sin)) return DSPARK_ERR_NULL;
+    if (dspark_status st = check_paged(k_cache, v_cache, cache_type, pages, page_size, page_stride,
+                                       head_stride, slot_stride, k_scale, v_scale, table_width, B,
+                                       rows, Hq, Hkv, D, 1024))
+        return st;
+    if (positions < 1 || half < 0 || 2 * (long long)half > D) return DSPARK_ERR_SHAPE;
+    if (q_stride < 0 || k_stride < 0 || v_stride < 0) return DSPARK_ERR_ARG;
+    if (misaligned(q, 2) || misaligned(k, 2) || misaligned(v, 2) || misaligned(q_out, 2) ||
+        misaligned(cos, 4) || misaligned(sin, 4) || misaligned(cu_seqlens, 4) ||
+        misaligned(ctx_lens, 4) || misaligned(block_table, 4))
+        return DSPARK_ERR_ALIGN;
+    AppendParams p;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.cos = cos;
+    p.sin = sin;
+    p.positions = positions;
+    p.half = half;
+    p.cu = cu_seqlens;
+    p.ctx = ctx_lens;
+    p.B = B;
+    p.rows = rows;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    const bool e4m3 = cache_type == DSPARK_CACHE_E4M3;
+    p.c = paged(k_cache, v_cache, pages, page_size, page_stride, head_stride, slot_stride, k_scale,
+                v_scale, e4m3, block_table, table_width);
+    p.out = q_out;
+    return launched(launch_append_kv(p, interleaved != 0, e4m3, as_stream(stream)));
+}
+
+DSPARK_API size_t dspark_attention_workspace_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
+    if (B < 1 || B > DSPARK_MAX_ROWS || max_rows < 1 || max_rows > DSPARK_MAX_ROWS || Hkv < 1 ||
+        Hq < Hkv || Hq % Hkv != 0 || Hq > kMaxHeads || D < 8 || D > 256 || D % 8 != 0)
+        return 0;
+    return attention_ws_bytes(B, max_rows, Hq, Hkv, D);
+}
+
+DSPARK_API dspark_status dspark_verify_attention(
+    const dspark_bf16 *q, long long q_row, long long q_head, const void *k_cache,
+    const void *v_cache, int cache_type, int pages, int page_size, long long page_stride,
+    long long head_stride, long long slot_stride, float k_scale, float v_scale,
+    const int32_t *block_table, int table_width, const int32_t *cu_seqlens,
+    const int32_t *ctx_lens, int B, int rows, int max_rows, int Hq, int Hkv, int D, int window,
+    float scale, dspark_bf16 *out, void *ws, size_t ws_bytes, void *stream) {
+    if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens || !ctx_lens || !out || !ws)
+        return DSPARK_ERR_NULL;
+    if (dspark_status st = check_paged(k_cache, v_cache, cache_type, pages, page_size, page_stride,
+                                       head_stride, slot_stride, k_scale, v_scale, table_width, B,
+                                       rows, Hq, Hkv, D, 256))
+        return st;
+    if (D % 8 != 0 || max_rows < 1) return DSPARK_ERR_SHAPE;
+    if (q_row < 0 || q_head < 0 || window < 0 || !std::isfinite(scale)) return DSPARK_ERR_ARG;
+    const bool e4m3 = cache_type == DSPARK_CACHE_E4M3;
+    const size_t item = e4m3 ? 1 : 2;
+    if (misaligned(q, 16) || misaligned(out, 16) || misaligned(ws, 16) || q_row % 8 != 0 ||
+        q_head % 8 != 0 || misaligned(k_cache, 8 * item) || misaligned(v_cache, 8 * item) ||
+        page_stride % 8 != 0 || head_stride % 8 != 0 || slot_stride % 8 != 0 ||
+        misaligned(block_table, 4) || misaligned(cu_seqlens, 4) || misaligned(ctx_lens, 4))
+        return DSPARK_ERR_ALIGN;
+    // a request has at most `rows` rows
+    max_rows = max_rows < rows ? max_rows : rows;
+    if (ws_bytes < attention_ws_bytes(B, max_rows, Hq, Hkv, D)) return DSPARK_ERR_WORKSPACE;
+    AttendParams p;
+    p.q = q;
+    p.q_row = q_row;
+    p.q_head = q_head;
+    p.cu = cu_seqlens;
+    p.ctx = ctx_lens;
+    p.B = B;
+    p.rows = rows;
+    p.max_rows = max_rows;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.window = window;
+    p.scale = scale;
+    p.c = paged(k_cache, v_cache, pages, page_size, page_stride, head_stride, slot_stride, k_scale,
+                v_scale, e4m3, block_table, table_width);
+    p.out = out;
+    return launched(launch_attention(p, e4m3, ws, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_sample_accept(
+    const dspark_bf16 *logits, const int32_t *packed_src_row, const int32_t *cu_seqlens,
+    const int32_t *tokens, const float *uniforms, const float *temperature, const int32_t *top_k,
+    const float *top_p, const float *min_p, int B, int gamma, int V, int32_t *packed_sample,
+    int32_t *accepted, int32_t *bonus, void *ws, size_t ws_bytes, void *stream) {
+    if (!logits || !cu_seqlens || !tokens || !uniforms || !packed_sample || !accepted || !bonus ||
+        !ws)
+        return DSPARK_ERR_NULL;
+    if (dspark_status st = check_bg(B, gamma)) return st;
+    if (V < 1) return DSPARK_ERR_SHAPE;
+    if (misaligned(logits, 2) || misaligned(packed_src_row, 4) || misaligned(cu_seqlens, 4) ||
+        misaligned(tokens, 4) || misaligned(uniforms, 4) || misaligned(temperature, 4) ||
+        misaligned(top_k, 4) || misaligned(top_p, 4) || misaligned(min_p, 4) ||
+        misaligned(packed_sample, 4) || misaligned(accepted, 4) || misaligned(bonus, 4) ||
+        misaligned(ws, 16))
+        return DSPARK_ERR_ALIGN;
+    if (ws_bytes < ws_total_bytes(B, gamma)) return DSPARK_ERR_WORKSPACE;
+    SampleParams p;
+    p.logits = logits;
+    p.psrc = packed_src_row;
+    p.cu = cu_seqlens;
+    p.tokens = tokens;
+    p.uniforms = uniforms;
+    p.temperature = temperature;
+    p.top_k = top_k;
+    p.top_p = top_p;
+    p.min_p = min_p;
+    p.B = B;
+    p.gamma = gamma;
+    p.V = V;
+    p.sample = packed_sample;
+    p.acc = accepted;
+    p.bonus = bonus;
+    return launched(launch_sample_accept(p, ws, as_stream(stream)));
 }

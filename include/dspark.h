@@ -358,6 +358,129 @@ dspark_status dspark_step_noalloc(const dspark_bf16 *hidden, const dspark_bf16 *
                                   int32_t *packed_argmax, int32_t *accepted, int32_t *bonus,
                                   int32_t *status, void *stream);
 
+/* ------------------------------------------------ around the verify forward
+ *
+ * The target's forward over the packed rows, per layer: dspark_append_kv
+ * (rotate queries and keys, write keys and values into the paged cache), then
+ * dspark_verify_attention; after the last layer, dspark_sample_accept draws
+ * the target's tokens where dspark_accept takes the largest logits.
+ *
+ * Packed rows: row r of request b is r = cu_seqlens[b] + j and stands at
+ * position ctx_lens[b] + j, where ctx_lens[b] counts the tokens that were in
+ * the cache before the call. One row per request is plain decoding, up to
+ * gamma + 1 are a verify window, any number a chunk of a prompt. `rows` is the
+ * capacity of the packed arrays; rows at and past cu_seqlens[B] are untouched.
+ *
+ * Paged cache: k_cache and v_cache hold `pages` pages of page_size slots for
+ * Hkv heads of D values. Element (page, head, slot, d) of either lies at
+ * page*page_stride + head*head_stride + slot*slot_stride + d (in elements), so
+ * any order of those axes and one pool for both are served. Position t of
+ * request b is slot t % page_size of page block_table[b*table_width +
+ * t / page_size]; an entry outside [0, pages) names no page: nothing is
+ * written there, and attention sees nothing there. cache_type: bf16, or e4m3
+ * (8 bits, finite up to 448) that stands for its value times k_scale or
+ * v_scale.
+ */
+typedef enum dspark_cache_type {
+    DSPARK_CACHE_BF16 = 0,
+    DSPARK_CACHE_E4M3 = 1
+} dspark_cache_type;
+
+/*
+ * Rotates the packed rows' queries and keys by their positions and writes keys
+ * and values into the paged cache, one pass over each. With (x1, x2) a pair of
+ * a head's first 2*half elements (elements i and half + i; with `interleaved`,
+ * 2i and 2i + 1) at position t:
+ *   y1 = x1*cos[t,i] - x2*sin[t,i],   y2 = x2*cos[t,i] + x1*sin[t,i]
+ * in fp32, rounded once to the nearest (ties to even) when stored. Elements
+ * from 2*half on, and values, are not rotated. Into an e4m3 cache go y / k_scale
+ * and v / v_scale, clamped to +-448 (NaN stays NaN); into a bf16 cache the
+ * scales are not applied.
+ * q [rows, Hq, D], k and v [rows, Hkv, D] bf16 with q_stride, k_stride and
+ * v_stride elements between rows and heads side by side (views of one fused
+ * projection are served); cos, sin [positions, half] fp32 (NULL is fine where
+ * half is 0: nothing is rotated); cu_seqlens [B+1],
+ * ctx_lens [B], block_table [B, table_width] int32; q_out [rows, Hq, D] bf16,
+ * which may be q itself where q_stride is Hq*D. Rows whose position is not
+ * below `positions` are untouched. No two rows of a call may share a slot.
+ * DSPARK_ERR_SHAPE: B, rows, Hq, Hkv, D, positions, pages, page_size or
+ * table_width below 1, half below 0 or above D/2, Hq not a multiple of Hkv, D above
+ * 1024, rows above DSPARK_MAX_ROWS; DSPARK_ERR_ARG: an unknown cache_type, a
+ * scale that is not finite and positive, a negative stride.
+ */
+dspark_status dspark_append_kv(const dspark_bf16 *q, const dspark_bf16 *k, const dspark_bf16 *v,
+                               long long q_stride, long long k_stride, long long v_stride,
+                               const float *cos, const float *sin, int positions, int half,
+                               int interleaved, const int32_t *cu_seqlens,
+                               const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv, int D,
+                               void *k_cache, void *v_cache, int cache_type, int pages,
+                               int page_size, long long page_stride, long long head_stride,
+                               long long slot_stride, float k_scale, float v_scale,
+                               const int32_t *block_table, int table_width, dspark_bf16 *q_out,
+                               void *stream);
+
+/*
+ * Attention of the packed rows over each request's pages, causal at the end of
+ * the request. A row at position t sees positions max(0, t - window + 1) .. t
+ * (from 0 when window is 0) that the table names:
+ *   out[r, h] = sum_s p_s V_s / sum_s p_s,  p_s = exp(scale * (q[r,h] . K_s) - max)
+ * with K and V of head h / (Hq / Hkv), statistics in fp32 and one rounding of
+ * the result to bf16. A row that sees no position gives zeros.
+ * q [rows, Hq, D] bf16, q_row and q_head elements between rows and heads;
+ * max_rows bounds the rows of a request (rows past it are untouched); out
+ * [rows, Hq, D] bf16, not overlapping q or the cache. D is a multiple of 8 up
+ * to 256. q, out, and the caches with all their strides are aligned to 16
+ * bytes (e4m3 caches to 8), else DSPARK_ERR_ALIGN. ws: at least
+ * dspark_attention_workspace_bytes(...) bytes, 16-byte aligned, zero-filled
+ * before its first use (dspark_workspace_init), shared by no two calls that
+ * overlap in time. Other checks as for dspark_append_kv, and DSPARK_ERR_ARG for
+ * a scale that is not finite or a negative window.
+ */
+dspark_status dspark_verify_attention(const dspark_bf16 *q, long long q_row, long long q_head,
+                                      const void *k_cache, const void *v_cache, int cache_type,
+                                      int pages, int page_size, long long page_stride,
+                                      long long head_stride, long long slot_stride, float k_scale,
+                                      float v_scale, const int32_t *block_table, int table_width,
+                                      const int32_t *cu_seqlens, const int32_t *ctx_lens, int B,
+                                      int rows, int max_rows, int Hq, int Hkv, int D, int window,
+                                      float scale, dspark_bf16 *out, void *ws, size_t ws_bytes,
+                                      void *stream);
+
+/* Scratch bytes of dspark_verify_attention for these sizes; 0 for invalid ones. */
+size_t dspark_attention_workspace_bytes(int B, int max_rows, int Hq, int Hkv, int D);
+
+/*
+ * Steps 5-6 with a drawn target token in the place of the largest logit. A
+ * packed row's entries are ranked by logit, largest first and lowest index
+ * first among equals (-0 and +0 are equal), and weigh w = exp((x - max) / T).
+ * In this order each filter keeps a prefix of what the one before it kept (at
+ * least one entry):
+ *   top_k[b] > 0:  the first top_k[b] entries;
+ *   top_p[b] < 1:  the entries whose preceding weight is below top_p[b] times
+ *                  the kept sum;
+ *   min_p[b] > 0:  the entries with w >= min_p[b];
+ * and packed_sample[r] is the first entry whose cumulated weight, itself
+ * included, exceeds uniforms[r] (in [0, 1)) times the kept sum. A temperature that
+ * is not above 0 takes the largest logit. NaN and -inf weigh nothing; a row of
+ * nothing else gives 0, its lowest index. +inf takes all the weight.
+ *   accepted[b], bonus[b]: as for dspark_accept, with packed_sample in the place
+ *   of packed_argmax.
+ * logits, packed_src_row (nullable), cu_seqlens and tokens as for
+ * dspark_accept; uniforms [B*(gamma+1)] fp32, one for every packed row;
+ * temperature, top_p, min_p [B] fp32 and top_k [B] int32, each nullable:
+ * temperature 1 and no filter. packed_sample [B*(gamma+1)], accepted and bonus
+ * [B] int32 outputs. A drawn token is exact: counts of equal logits are whole
+ * numbers and weights are summed in 64 bits. ws as for dspark_accept, and it
+ * may be the same one.
+ */
+dspark_status dspark_sample_accept(const dspark_bf16 *logits, const int32_t *packed_src_row,
+                                   const int32_t *cu_seqlens, const int32_t *tokens,
+                                   const float *uniforms, const float *temperature,
+                                   const int32_t *top_k, const float *top_p, const float *min_p,
+                                   int B, int gamma, int V, int32_t *packed_sample,
+                                   int32_t *accepted, int32_t *bonus, void *ws, size_t ws_bytes,
+                                   void *stream);
+
 /* Scratch bytes needed by dspark_accept and dspark_step for these sizes
  * (independent of d); 0 for invalid sizes. */
 size_t dspark_workspace_bytes(int B, int gamma, int V);

@@ -1,0 +1,232 @@
+"""Attention of the packed rows over the paged cache against its 64-bit
+definition (needs an MI355X): single tokens, verify windows and prompt chunks,
+head groups, types, page sizes, windows, strides, rows that see nothing, long
+contexts, graph replays."""
+import random
+
+import pytest
+import torch
+
+import __graft_entry__  # noqa: F401
+import confidence_scheduled_ragged_amd as dspark
+import forward_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def make(rows, ctx, Hq, Hkv, D, page, cache="bf16", seed=0, layout="page_head", q_pad=0,
+         spread=1.5, spare=3):
+    gen = torch.Generator().manual_seed(seed)
+    B = len(rows)
+    cu = [0]
+    for n in rows:
+        cu.append(cu[-1] + n)
+    need = [-(-(max(c, 0) + n) // page) for c, n in zip(ctx, rows)]
+    pages = sum(need) + spare
+    perm = torch.randperm(pages, generator=gen).to(torch.int32)
+    table = torch.full((B, max(need) + 1), -1, dtype=torch.int32)
+    used = 0
+    for b in range(B):
+        table[b, :need[b]] = perm[used:used + need[b]]
+        used += need[b]
+    cap = cu[-1] + 3
+    q = (torch.randn((cap, Hq, D + q_pad), generator=gen) * spread).bfloat16()
+    shape = (pages, Hkv, page, D) if layout == "page_head" else (pages, page, Hkv, D)
+    mul = 30.0 if cache == "e4m3" else 1.0
+    kc, vc = ((torch.randn(shape, generator=gen) * mul).clamp(-448, 448) for _ in range(2))
+    dtype = torch.float8_e4m3fn if cache == "e4m3" else torch.bfloat16
+    kc, vc = kc.to(dtype), vc.to(dtype)
+    return dict(q=q, D=D, kc=kc, vc=vc, cu=cu, ctx=list(ctx), table=table, layout=layout,
+                max_rows=max(max(rows), 1), cap=cap, Hq=Hq)
+
+
+def to_dev(x):
+    if x.dtype == torch.float8_e4m3fn:
+        return x.view(torch.uint8).to(DEV).view(torch.float8_e4m3fn)
+    return x.to(DEV)
+
+
+def pools(c, dev):
+    kc, vc = (to_dev(c["kc"]), to_dev(c["vc"])) if dev == DEV else (c["kc"], c["vc"])
+    return (kc, vc) if c["layout"] == "page_head" else (kc.transpose(1, 2), vc.transpose(1, 2))
+
+
+def call(c, kc, vc, out, **kw):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    q = c["q"].to(DEV)[:, :, :c["D"]]
+    return dspark.dspark_verify_attention(q, kc, vc, i32(c["cu"]), i32(c["ctx"]),
+                                          c["table"].to(DEV), c["max_rows"], out=out, **kw)
+
+
+def check(c, **kw):
+    kc, vc = pools(c, "cpu")
+    out = torch.randn((c["cap"], c["Hq"], c["D"])).bfloat16()
+    want, tol = ref.attend(c["q"][:, :, :c["D"]], kc, vc, c["cu"], c["ctx"], c["table"],
+                           c["max_rows"], out=out, **kw)
+    got = call(c, *pools(c, DEV), out.to(DEV), **kw)
+    torch.cuda.synchronize()
+    got = got.cpu().double()
+    assert not bool(torch.isnan(got).any())
+    off = (got - want).abs()
+    bad = off > tol
+    assert not bool(bad.any()), (int(bad.sum()), float(off.max()),
+                                 [int(i) for i in bad.nonzero()[0]])
+    return got
+
+
+SCALES = dict(bf16={}, e4m3=dict(k_scale=0.03125, v_scale=0.0234375))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", [
+    (8, 2, 128, 16), (5, 1, 64, 32), (6, 3, 64, 64), (4, 4, 128, 128), (8, 1, 128, 64),
+    (3, 1, 80, 16), (2, 1, 256, 16), (2, 2, 8, 16), (4, 2, 96, 24), (2, 1, 128, 1), (4, 1, 64, 7)])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_verify_windows(Hq, Hkv, D, page, cache):
+    rows, ctx = [1, 17, 4, 0, 2, 9], [0, 300, 63, 10, 1, 129]
+    check(make(rows, ctx, Hq, Hkv, D, page, cache, seed=D + Hq), **SCALES[cache])
+
+
+@pytest.mark.parametrize("ctx", [0, 1, 15, 16, 31, 32, 63, 64, 127, 128, 1000, 4097])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_single_token(ctx, cache):
+    check(make([1], [ctx], 8, 2, 128, 16, cache, seed=ctx), **SCALES[cache])
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (128, 5), (64, 8)])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_prompts(D, G, cache):
+    check(make([150, 1, 64, 257], [0, 0, 0, 0], 2 * G, 2, D, 16, cache, seed=G), **SCALES[cache])
+
+
+@pytest.mark.parametrize("D,G,page", [(64, 2, 64), (128, 8, 16), (128, 3, 32)])
+def test_chunks_on_a_cached_prefix(D, G, page):
+    check(make([130, 70], [333, 1001], G, 1, D, page, seed=G + D))
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 100, 1000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_windows(window, D):
+    check(make([17, 1, 5, 140], [500, 2000, 7, 90], 4, 2, D, 32, seed=window), window=window)
+    check(make([1, 1], [700, 3], 4, 2, D, 16, "e4m3", seed=window), window=window,
+          **SCALES["e4m3"])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_other_axis_order_and_strided_queries(D, cache):
+    check(make([3, 1, 40], [40, 100, 0], 8, 2, D, 16, cache, seed=1, layout="page_slot", q_pad=64),
+          **SCALES[cache])
+
+
+@pytest.mark.parametrize("rows", [[1, 1, 1, 1], [17, 3, 17, 3], [100, 2, 90, 3]])
+def test_pages_the_table_does_not_name(rows):
+    c = make(rows, [100, 100, 5, 200], 4, 2, 128, 16, seed=2)
+    pages = c["kc"].shape[0]
+    c["table"][0, 2] = -1
+    c["table"][1, :] = pages          # nothing to see: zeros
+    c["table"][2, 0] = pages + 5
+    c["table"][3, 3:6] = -9
+    got = check(c)
+    r = c["cu"][1]
+    assert float(got[r:r + rows[1]].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("D", [64, 128, 96])
+def test_what_is_not_seen_may_hold_anything(D):
+    """NaN and infinities in slots after a request's end, in slots before the
+    window and in pages of nobody change nothing."""
+    c = make([5, 1, 33], [59, 70, 30], 4, 2, D, 16, seed=3)
+    kw = dict(window=40)
+    clean = check(c, **kw)
+    live = torch.zeros(c["kc"].shape[0], c["kc"].shape[2], dtype=torch.bool)
+    for b in range(3):
+        n = c["cu"][b + 1] - c["cu"][b]
+        for t in range(max(0, c["ctx"][b] + 1 - 40), c["ctx"][b] + n):
+            live[int(c["table"][b, t // 16]), t % 16] = True
+    for x, bad in ((c["kc"], float("nan")), (c["vc"], float("inf"))):
+        x.copy_(torch.where(live[:, None, :, None], x, torch.full_like(x, bad)))
+    kc, vc = pools(c, DEV)
+    out = torch.zeros((c["cap"], c["Hq"], c["D"]), dtype=torch.bfloat16, device=DEV)
+    got = call(c, kc, vc, out, **kw).cpu().double()
+    assert torch.equal(got[:c["cu"][-1]], clean[:c["cu"][-1]])
+
+
+def test_large_scores():
+    """Scores far apart and far from zero: the running maximum carries them."""
+    c = make([9, 1], [300, 900], 4, 2, 128, 16, seed=4, spread=100.0)
+    check(c)
+    check(make([9, 1], [300, 900], 4, 2, 64, 16, seed=5), scale=0.0)
+
+
+def test_lengths_the_kernels_bound():
+    """A context of less than none, a table shorter than the context, more rows
+    than max_rows: clamped, nothing else touched."""
+    c = make([4, 6, 5], [-3, 60, 33], 4, 2, 128, 16, seed=6)
+    c["max_rows"] = 4
+    c["table"] = c["table"][:, :4].contiguous()
+    check(c)
+
+
+def test_a_long_context_split_over_the_device():
+    check(make([1], [30011], 4, 1, 128, 16, "e4m3", seed=7), **SCALES["e4m3"])
+    check(make([3], [20000], 2, 2, 64, 64, seed=8))
+
+
+def test_many_requests():
+    rng = random.Random(9)
+    rows = [rng.choice((1, 1, 2, 5, 17)) for _ in range(160)]
+    ctx = [rng.randint(0, 200) for _ in rows]
+    check(make(rows, ctx, 2, 1, 64, 16, seed=9))
+
+
+def test_repeats_are_equal_and_on_another_stream():
+    c = make([17, 1, 5], [3000, 900, 40], 8, 2, 128, 16, seed=10)
+    kc, vc = pools(c, DEV)
+    a = call(c, kc, vc, None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = call(c, kc, vc, None)
+    torch.cuda.synchronize()
+    assert torch.equal(a[:c["cu"][-1]], b[:c["cu"][-1]])
+
+
+def test_graph_replays_with_new_lengths():
+    """A captured call follows the lengths in its buffers."""
+    c = make([17, 1, 5, 3], [900, 2000, 40, 0], 8, 2, 128, 16, seed=11)
+    kc, vc = pools(c, DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    q, cu, ctx, table = c["q"].to(DEV), i32(c["cu"]), i32(c["ctx"]), c["table"].to(DEV)
+    out = torch.zeros((c["cap"], 8, 128), dtype=torch.bfloat16, device=DEV)
+
+    def body():
+        dspark.dspark_verify_attention(q, kc, vc, cu, ctx, table, 17, out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        body()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    for rows, lens in (([17, 1, 5, 3], [900, 2000, 40, 0]), ([1, 1, 1, 1], [5, 1000, 44, 2]),
+                       ([3, 1, 17, 5], [20, 7, 28, 1])) * 2:
+        starts = [0]
+        for n in rows:
+            starts.append(starts[-1] + n)
+        cu.copy_(i32(starts))
+        ctx.copy_(i32(lens))
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        out.fill_(7)
+        body()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+        want, tol = ref.attend(c["q"], c["kc"], c["vc"], starts, lens, c["table"], 17,
+                               out=torch.full(out.shape, 7.0).bfloat16())
+        assert bool(((got.cpu().double() - want).abs() <= tol).all())
