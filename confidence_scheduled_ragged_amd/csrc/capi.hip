@@ -423,6 +423,7 @@ dspark_status check_paged(const void *k_cache, const void *v_cache, int cache_ty
     if (B < 1 || rows < 1 || rows > DSPARK_MAX_ROWS || B > DSPARK_MAX_ROWS) return DSPARK_ERR_SHAPE;
     if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > kMaxHeads) return DSPARK_ERR_SHAPE;
     if (D < 1 || D > max_d || pages < 1 || page_size < 1 || table_width < 1) return DSPARK_ERR_SHAPE;
+    if ((long long)rows * Hq > 0x7FFFFFFFll) return DSPARK_ERR_SHAPE;
     // positions are 32-bit
     if ((long long)table_width * page_size > 0x7FFFFFFFll) return DSPARK_ERR_SHAPE;
     if (cache_type != DSPARK_CACHE_BF16 && cache_type != DSPARK_CACHE_E4M3) return DSPARK_ERR_ARG;
