@@ -22,26 +22,36 @@ constexpr int kSampleThreads = 512;
 constexpr int kSampleWaves = kSampleThreads / kWave;
 constexpr int kSampleWavesPerSimd = 6;  // three workgroups a CU
 constexpr int kRowUnroll = 8;  // 16-byte loads in flight per lane
+constexpr int kWideUnroll = 2;
+constexpr int kListed = 1024;  // equals that are ranked by their indices
 
-// Places. A value's place counts down the ranking; 64 places are a block.
+// Places. A value's place counts down the ranking; 256 places are a block, four
+// to a lane, so that one ballot finds a block of the 49 narrow ones.
 //
 // Narrow places: |x| in [2^-32, 2^16), 128 values an octave and a sign, one
-// place each, with a place for what is larger or smaller at every end. The
-// counters of all of them take 48 KiB of LDS, so three workgroups share a CU
-// and one's loads run beside another's atomics. The end places hold more than
-// one value, so a row is finished this way only if they do not matter: nothing
-// at or above 2^16, nothing nonzero below 2^-32, and what lies at or below
-// -2^16 (masks, -inf) so far down that it weighs nothing (kNegligible).
+// place each, one more at either side of zero for what is smaller, and 64 at
+// either end for what is larger, so that the lanes of a masked vocabulary do not
+// meet at one. The counters of all of them take 49 KiB of LDS: three workgroups
+// share a CU, and one's loads run beside another's atomics. A counter holds 16
+// bits for each half of the row, so that the drawn entry is then looked for in
+// its half only: HBM is read one and a half times. The end places and the two at
+// zero hold more than one value, so a row is finished this way only if that does
+// not matter: nothing at or above 2^16, nothing nonzero below 2^-32, what lies
+// at or below -2^16 (masks, -inf) so far down that it weighs nothing
+// (kNegligible), and no counter over 16 bits (the counts add up to V).
 //
 // Wide places: every bf16 value, 65536 places, counted in eight rounds over
 // the row. Any row can be finished this way.
 constexpr uint32_t kNarrowLo = (127 - 32) << 7, kNarrowHi = (127 + 16) << 7;  // bits of |x|
 constexpr int kNarrowSpan = (int)(kNarrowHi - kNarrowLo);
-constexpr int kPlaceZero = kNarrowSpan + 1;  // +0 and what is below 2^-32
-constexpr int kPlaceMinus = kPlaceZero + 1;  // -0 and what is above -2^-32
-constexpr int kPlaceLow = kPlaceMinus + kNarrowSpan + 1;  // -2^16 and below, NaN
-constexpr int kNarrowBlocks = (kPlaceLow + kWave) / kWave;
-constexpr int kWideBlocks = 1024;
+constexpr int kPlaceZero = kWave + kNarrowSpan;  // +0 and what is below 2^-32
+constexpr int kPlaceMinus = kPlaceZero + 1;      // -0 and what is above -2^-32
+constexpr int kPlaceLow = kPlaceMinus + kNarrowSpan + 1;  // 64 places: -2^16 and below, NaN
+constexpr uint32_t kFirstHalf = 1u, kSecondHalf = 1u << 16;
+constexpr int kPer = 4;  // places of a lane
+constexpr int kBlock = kPer * kWave;
+constexpr int kNarrowBlocks = (kPlaceLow + kWave + kBlock - 1) / kBlock;
+constexpr int kWideBlocks = 65536 / kBlock;
 constexpr int kWideRound = 8192;  // counters of one round
 // exp(-60) of the largest weight times 2^31 entries is 2e-17 of the sum, below
 // the half step of the 64-bit sums.
@@ -49,21 +59,23 @@ constexpr double kNegligible = 60.0;
 
 struct Narrow {
     static constexpr int kBlocks = kNarrowBlocks;
-    uint32_t bins[kBlocks * kWave];
+    uint32_t bins[kBlocks * kBlock];
     double wex[kBlocks + 1];  // weight and count before each block
     int cex[kBlocks + 1];
+    __device__ static int count(uint32_t c) { return (int)((c & 0xFFFFu) + (c >> 16)); }
     // bits of the value at a place
     __device__ static uint32_t bits(int e) {
         e = e > kPlaceLow ? kPlaceLow : e;
         if (e == kPlaceZero || e == kPlaceMinus) return 0u;
-        return e < kPlaceZero ? kNarrowHi - (uint32_t)e
+        return e < kPlaceZero ? kNarrowHi - 1u - (uint32_t)(e - kWave)
                               : 0x8000u | (kNarrowLo - 1u + (uint32_t)(e - kPlaceMinus));
     }
 };
 struct Wide {
     static constexpr int kBlocks = kWideBlocks;
+    __device__ static int count(uint32_t c) { return (int)c; }
     uint32_t bins[kWideRound];
-    uint32_t detail[kWave];  // counts of the block at hand
+    uint32_t detail[kBlock];  // counts of the block at hand
     double wex[kBlocks + 1];
     int cex[kBlocks + 1];
     __device__ static uint32_t bits(int e) {
@@ -71,12 +83,14 @@ struct Wide {
         return key & 0x8000u ? key ^ 0x8000u : ~key & 0xFFFFu;
     }
 };
-struct SampleLds {
+struct alignas(16) SampleLds {
     union {
         Narrow narrow;
         Wide wide;
     };
     int part[kSampleWaves];
+    int listed;    // entries found of the drawn value
+    int counted;   // entries in the narrow places above kPlaceLow
     unsigned top;  // place of the largest value that counts
     int flag, at;
 };
@@ -98,6 +112,8 @@ struct Row {
         head = head < n ? head : n;
         vecs = (n - head) / 8;
     }
+    // vectors of the row's first half, where the head belongs too
+    __device__ int half() const { return vecs / 2; }
     __device__ int loose() const { return V - 8 * vecs; }
     // index of the i-th entry outside the vectors
     __device__ int loose_at(int i) const { return i < head ? i : 8 * vecs + i; }
@@ -106,30 +122,30 @@ struct Row {
 
 // f(vector, its number) for vectors [v0, v1), by lanes `step` apart, the first
 // of them at v0 + lane; f must take lanes that are off.
-template <typename F>
+template <int kUnroll = kRowUnroll, typename F>
 __device__ __forceinline__ void for_vecs(const Row &row, int v0, int v1, int lane, int step, F f) {
     const u32x4 *at = row.vec();
     int v = v0 + lane;
-    for (; v + (kRowUnroll - 1) * step < v1; v += kRowUnroll * step) {
-        u32x4 a[kRowUnroll];
+    for (; v + (kUnroll - 1) * step < v1; v += kUnroll * step) {
+        u32x4 a[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kRowUnroll; ++i) a[i] = at[v + i * step];
+        for (int i = 0; i < kUnroll; ++i) a[i] = at[v + i * step];
 #pragma unroll
-        for (int i = 0; i < kRowUnroll; ++i) f(a[i], v + i * step);
+        for (int i = 0; i < kUnroll; ++i) f(a[i], v + i * step);
     }
     if (v < v1) {  // the last round's loads past the end repeat its first
-        u32x4 a[kRowUnroll];
+        u32x4 a[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kRowUnroll; ++i) a[i] = at[v + i * step < v1 ? v + i * step : v];
+        for (int i = 0; i < kUnroll; ++i) a[i] = at[v + i * step < v1 ? v + i * step : v];
 #pragma unroll
-        for (int i = 0; i < kRowUnroll; ++i)
+        for (int i = 0; i < kUnroll; ++i)
             if (v + i * step < v1) f(a[i], v + i * step);
     }
 }
 // f(bits) for every entry of the row, by the whole workgroup.
 template <typename F>
 __device__ __forceinline__ void for_row(const Row &row, F f) {
-    for_vecs(row, 0, row.vecs, threadIdx.x, kSampleThreads, [&](u32x4 a, int) {
+    for_vecs<kWideUnroll>(row, 0, row.vecs, threadIdx.x, kSampleThreads, [&](u32x4 a, int) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             f(a[i] & 0xFFFFu);
@@ -139,19 +155,24 @@ __device__ __forceinline__ void for_row(const Row &row, F f) {
     if ((int)threadIdx.x < row.loose()) f((uint32_t)row.p[row.loose_at(threadIdx.x)]);
 }
 
-// Byte offsets of the counters of two values' narrow places, packed.
+// Byte offsets of the counters of two values' narrow places, packed: seven
+// instructions for two values (a 16-bit shift of both signs at once is not
+// found by the compiler). `end` is the lane's distance to its end places.
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef short i16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t narrow_offsets(uint32_t two) {
-    constexpr unsigned short lo = kNarrowLo - 1, hi = kNarrowHi;
-    const u16x2 x = __builtin_bit_cast(u16x2, two);
+__device__ __forceinline__ u16x2 narrow_end() {
+    const unsigned short e = (unsigned short)(kNarrowSpan + 1 + (threadIdx.x & (kWave - 1)));
+    return u16x2{e, e};
+}
+__device__ __forceinline__ uint32_t narrow_offsets(uint32_t two, u16x2 end) {
+    constexpr unsigned short lo = kNarrowLo - 1, c = 4 * kPlaceMinus;
     u16x2 m = __builtin_bit_cast(u16x2, two & 0x7FFF7FFFu);
-    m = __builtin_elementwise_max(m, (u16x2){lo, lo});
-    m = __builtin_elementwise_min(m, (u16x2){hi, hi}) - (u16x2){lo, lo};
+    m = __builtin_elementwise_min(__builtin_elementwise_sub_sat(m, (u16x2){lo, lo}),
+                                  end);
     // the place is kPlaceZero - m for a positive value, kPlaceMinus + m for a negative one
-    const u16x2 sign = __builtin_bit_cast(u16x2, __builtin_bit_cast(i16x2, x) >> 15);
-    const u16x2 e = (u16x2){kPlaceMinus, kPlaceMinus} + (m ^ ~sign);
-    return __builtin_bit_cast(uint32_t, (u16x2)(e << 2));
+    uint32_t sign;
+    asm("v_pk_ashrrev_i16 %0, 15, %1 op_sel_hi:[0,1]" : "=v"(sign) : "v"(two));
+    const u16x2 e = __builtin_bit_cast(u16x2, ~(__builtin_bit_cast(uint32_t, m) ^ sign));
+    return __builtin_bit_cast(uint32_t, (u16x2)(e * (u16x2){4, 4} + (u16x2){c, c}));
 }
 
 // Inclusive sum over the wave, lane 0 first, by the DPP moves of wave_incl_scan.
@@ -178,24 +199,25 @@ __device__ __forceinline__ double last_lane(double x) {
 __device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, kWave - 1); }
 
 struct Draw {
-    double T, u, top_p, min_p;
+    double T, per_T, u, top_p, min_p;  // per_T = 1 / T
     int k;
 };
-// What a row draws: the bits of its value, and which of its n equals.
+// What a row draws: the bits of its value, which of its equals, and its place.
 struct Drawn {
     uint32_t bits;
-    int j, n;
+    int j, place;
 };
 
 // Counts and weights of all blocks are in place (prefix sums in wex and cex,
 // totals at their ends); every wave walks the filters by itself, with the
-// same numbers. counts(t) gives lane l the count of place 64*t + l.
+// same numbers. counts(t) gives lane l the counts of places kBlock*t + kPer*l on.
 template <typename H, typename Weight, typename Counts>
 __device__ __forceinline__ Drawn walk_filters(const H &h, const Draw &d, Weight weight,
                                               Counts counts) {
     const int lane = threadIdx.x & (kWave - 1);
     // the first block for which `test` holds, -1 if none
     auto first = [&](auto test) {
+#pragma unroll 1
         for (int i0 = 0; i0 < H::kBlocks; i0 += kWave) {
             const int i = i0 + lane;
             const uint64_t m = __ballot(i < H::kBlocks && test(i));
@@ -203,17 +225,31 @@ __device__ __forceinline__ Drawn walk_filters(const H &h, const Draw &d, Weight 
         }
         return -1;
     };
-    // count and weight of this lane's place in block t, and what precedes it
-    int n = 0, before = 0, have = -1;
-    double w = 0.0, ahead = 0.0;
+    // counts and weights of this lane's places in block t, and what precedes them
+    int n[kPer] = {}, before[kPer] = {}, have = -1;
+    double w[kPer] = {}, ahead[kPer] = {};
     auto open = [&](int t) {
         if (t == have) return;
         have = t;
-        n = counts(t);
-        w = n ? weight(t * kWave + lane) : 0.0;
-        before = h.cex[t] + wave_incl_scan(n, lane) - n;
-        const double x = (double)n * w;
-        ahead = h.wex[t] + (wave_incl_sum(x) - x);
+        const u32x4 c = counts(t);
+        int sum = 0;
+        double x = 0.0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            n[u] = H::count(c[u]);
+            w[u] = n[u] ? weight(t * kBlock + kPer * lane + u) : 0.0;
+            before[u] = sum;
+            ahead[u] = x;
+            sum += n[u];
+            x += (double)n[u] * w[u];
+        }
+        const int b0 = h.cex[t] + wave_incl_scan(sum, lane) - sum;
+        const double a0 = h.wex[t] + (wave_incl_sum(x) - x);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            before[u] += b0;
+            ahead[u] += a0;
+        }
     };
     auto wave_sum = [&](int x) { return last_lane(wave_incl_scan(x, lane)); };
     int N = h.cex[H::kBlocks];
@@ -223,10 +259,44 @@ __device__ __forceinline__ Drawn walk_filters(const H &h, const Draw &d, Weight 
         if (keep >= N) return;
         const int t = first([&](int i) { return h.cex[i + 1] >= keep; });
         open(t);
-        int mine = keep - before;
-        mine = mine < 0 ? 0 : (mine > n ? n : mine);
-        total = h.wex[t] + last_lane(wave_incl_sum((double)mine * w));
+        double x = 0.0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            int mine = keep - before[u];
+            mine = mine < 0 ? 0 : (mine > n[u] ? n[u] : mine);
+            x += (double)mine * w[u];
+        }
+        total = h.wex[t] + last_lane(wave_incl_sum(x));
         N = keep;
+    };
+    // Entries of the open block that come before `goal`: of a place the first m
+    // with ahead + (m - 1) w below it or, `whole`, with ahead + m w at most it.
+    // One place at most holds the border; only there m is searched for.
+    auto entries = [&](double goal, bool whole) {
+        auto in = [&](double a, double x, int m) {
+            return whole ? a + (double)m * x <= goal : a + (double)(m - 1) * x < goal;
+        };
+        int sum = 0, c = 0;
+        double a = 0.0, x = 0.0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            if (n[u] == 0 || !in(ahead[u], w[u], 1)) continue;
+            if (in(ahead[u], w[u], n[u])) {
+                sum += n[u];
+            } else {
+                c = n[u];
+                a = ahead[u];
+                x = w[u];
+            }
+        }
+        if (c) {
+            const double q = (goal - a) / x;
+            int m = q < 1.0 ? 1 : (q < (double)c ? (int)q : c);
+            while (m > 1 && !in(a, x, m)) --m;
+            while (m < c && in(a, x, m + 1)) ++m;
+            sum += m;
+        }
+        return wave_sum(sum);
     };
     if (d.k > 0) cut(d.k);
     if (d.top_p < 1.0) {
@@ -236,17 +306,7 @@ __device__ __forceinline__ Drawn walk_filters(const H &h, const Draw &d, Weight 
         }) : -1;
         if (t >= 0) {
             open(t);
-            int m = 0;
-            if (n && ahead < goal) {
-                m = n;
-                if (w > 0.0) {
-                    const double q = ceil((goal - ahead) / w);
-                    m = q < (double)n ? (int)q : n;
-                    while (m > 0 && !(ahead + (double)(m - 1) * w < goal)) --m;
-                    while (m < n && ahead + (double)m * w < goal) ++m;
-                }
-            }
-            cut(h.cex[t] + wave_sum(m));
+            cut(h.cex[t] + entries(goal, false));
         } else if (!(goal > 0.0)) {
             cut(1);
         }
@@ -254,11 +314,14 @@ __device__ __forceinline__ Drawn walk_filters(const H &h, const Draw &d, Weight 
     if (d.min_p > 0.0) {
         // the first block that is not kept whole
         const int t = first([&](int i) {
-            return h.cex[i + 1] > h.cex[i] && !(weight(i * kWave + kWave - 1) >= d.min_p);
+            return h.cex[i + 1] > h.cex[i] && !(weight(i * kBlock + kBlock - 1) >= d.min_p);
         });
         if (t >= 0) {
             open(t);
-            cut(h.cex[t] + wave_sum(n && w >= d.min_p ? n : 0));
+            int m = 0;
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) m += n[u] && w[u] >= d.min_p ? n[u] : 0;
+            cut(h.cex[t] + wave_sum(m));
         }
     }
     const double goal = d.u * total;
@@ -268,36 +331,49 @@ __device__ __forceinline__ Drawn walk_filters(const H &h, const Draw &d, Weight 
     });
     if (t >= 0) {
         open(t);
-        int m = 0;
-        if (n && w > 0.0) {
-            const double q = floor((goal - ahead) / w);
-            m = q < 0.0 ? 0 : (q < (double)n ? (int)q : n);
-            while (m > 0 && !(ahead + (double)m * w <= goal)) --m;
-            while (m < n && ahead + (double)(m + 1) * w <= goal) ++m;
-        }
-        const int x = h.cex[t] + wave_sum(m);
+        const int x = h.cex[t] + entries(goal, true);
         rank = x < rank ? x : rank;
     }
     const int at = first([&](int i) { return h.cex[i + 1] > rank; });
     open(at);
-    const uint64_t mine = __ballot(before <= rank && rank < before + n);
-    const int l = __ffsll((unsigned long long)mine) - 1;
+    int place = 0, nth = 0;
+    bool mine = false;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        if (before[u] <= rank && rank < before[u] + n[u]) {
+            mine = true;
+            place = at * kBlock + kPer * lane + u;
+            nth = rank - before[u];
+        }
+    }
+    const int l = __ffsll((unsigned long long)__ballot(mine)) - 1;
     Drawn r;
-    r.bits = H::bits(at * kWave + l);
-    r.n = __builtin_amdgcn_readlane(n, l);
-    r.j = rank - __builtin_amdgcn_readlane(before, l);
+    r.place = __builtin_amdgcn_readlane(place, l);
+    r.bits = H::bits(r.place);
+    r.j = __builtin_amdgcn_readlane(nth, l);
     return r;
 }
 
-// Count and weight of block i from this lane's counter.
+// Count and weight of block i from its counters; a lane's four exponentials run
+// side by side.
 template <typename H, typename Weight>
-__device__ __forceinline__ void sum_block(H &h, int i, uint32_t n, Weight weight) {
+__device__ __forceinline__ void sum_block(H &h, int i, const uint32_t *bins, Weight weight) {
     const int lane = threadIdx.x & (kWave - 1);
+    const u32x4 n = reinterpret_cast<const u32x4 *>(bins)[lane];
     int c = 0;
     double w = 0.0;
-    if (__ballot(n != 0)) {
-        c = last_lane(wave_incl_scan((int)n, lane));
-        w = last_lane(wave_incl_sum(n ? (double)n * weight(i * kWave + lane) : 0.0));
+    if (__ballot((n[0] | n[1] | n[2] | n[3]) != 0)) {
+        double x[kPer];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) x[u] = weight(i * kBlock + kPer * lane + u);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int k = H::count(n[u]);
+            c += k;
+            w += k ? (double)k * x[u] : 0.0;
+        }
+        c = last_lane(wave_incl_scan(c, lane));
+        w = last_lane(wave_incl_sum(w));
     }
     if (lane == 0) {
         h.cex[i] = c;
@@ -310,6 +386,7 @@ __device__ __forceinline__ void scan_blocks(H &h) {
     const int lane = threadIdx.x & (kWave - 1);
     int c0 = 0;
     double w0 = 0.0;
+#pragma unroll 1
     for (int i0 = 0; i0 < H::kBlocks; i0 += kWave) {
         const int i = i0 + lane;
         const int c = i < H::kBlocks ? h.cex[i] : 0;
@@ -331,46 +408,57 @@ __device__ __forceinline__ void scan_blocks(H &h) {
     }
 }
 
-// The index of the (j+1)-th of the row's n entries that equal `bits` (zeros of
-// either sign are equal).
-__device__ __forceinline__ int index_of(SampleLds &s, const Row &row, const Drawn &d) {
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const uint32_t mask = d.bits == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu;
-    const uint32_t want = d.bits | (d.bits << 16);
-    auto equal = [&](uint32_t x) { return (x & mask & 0xFFFFu) == d.bits; };
-    // a bit per entry; the usual vector holds none and costs 4 steps per word
-    auto matches = [&](u32x4 a) {
-        uint32_t t[4], some = 0;
+// Which entries equal a value (zeros of either sign are equal: kZero).
+template <bool kZero>
+struct Equal {
+    static constexpr uint32_t kMask = kZero ? 0x7FFF7FFFu : 0xFFFFFFFFu;
+    uint32_t want;
+    __device__ explicit Equal(uint32_t bits) : want(bits | (bits << 16)) {}
+    __device__ __forceinline__ bool one(uint32_t x) const {
+        return ((x ^ want) & kMask & 0xFFFFu) == 0;
+    }
+    // a bit per entry of a vector; the usual one holds none, which the smallest
+    // of the eight differences shows
+    __device__ __forceinline__ uint32_t vec(u32x4 a) const {
+        uint32_t t[4];
+        u16x2 least = {0xFFFF, 0xFFFF};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            t[i] = (a[i] & mask) ^ want;
-            some |= (t[i] - 0x00010001u) & ~t[i] & 0x80008000u;
+            t[i] = (a[i] ^ want) & kMask;
+            least = __builtin_elementwise_min(least, __builtin_bit_cast(u16x2, t[i]));
         }
         uint32_t m = 0;
-        if (some) {
+        if (least[0] == 0 || least[1] == 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 m |= ((t[i] & 0xFFFFu) == 0 ? 1u << (2 * i) : 0u) |
                      (t[i] >> 16 == 0 ? 2u << (2 * i) : 0u);
         }
         return m;
-    };
-    const bool edge = tid < row.loose() && equal(row.p[row.loose_at(tid)]);
-    if (d.n == 1) {
-        if (edge) s.at = row.loose_at(tid);
-        for_vecs(row, 0, row.vecs, tid, kSampleThreads, [&](u32x4 a, int v) {
-            const uint32_t m = matches(a);
-            if (m) s.at = row.head + 8 * v + __ffs((int)m) - 1;
-        });
-        __syncthreads();
-        return s.at;
     }
-    // a contiguous share of the vectors per wave
-    const int per = (row.vecs + kSampleWaves - 1) / kSampleWaves;
-    const int v0 = wave * per < row.vecs ? wave * per : row.vecs;
-    const int v1 = v0 + per < row.vecs ? v0 + per : row.vecs;
+};
+
+// The vectors of wave w: a contiguous share, in steps of a wave.
+struct Share {
+    int v0, v1;
+    __device__ Share(const Row &row, int w) {
+        const int per = (row.vecs + kSampleWaves * kWave - 1) / (kSampleWaves * kWave) * kWave;
+        v0 = w * per < row.vecs ? w * per : row.vecs;
+        v1 = v0 + per < row.vecs ? v0 + per : row.vecs;
+    }
+};
+
+// The index of the (j+1)-th of the row's entries that equal the drawn value, by
+// reading the row again.
+template <bool kZero>
+__device__ __forceinline__ int index_of(SampleLds &s, const Row &row, const Drawn &d) {
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const Equal<kZero> equal(d.bits);
+    const bool edge = tid < row.loose() && equal.one(row.p[row.loose_at(tid)]);
+    const Share mine(row, wave);
     int c = 0;
-    for_vecs(row, v0, v1, lane, kWave, [&](u32x4 a, int) { c += __popc(matches(a)); });
+    for_vecs(row, mine.v0, mine.v1, lane, kWave,
+             [&](u32x4 a, int) { c += __popc(equal.vec(a)); });
     c = last_lane(wave_incl_scan(c, lane));
     if (lane == 0) s.part[wave] = c;
     // the loose entries are all in the first wave: those of the head come first,
@@ -389,8 +477,8 @@ __device__ __forceinline__ int index_of(SampleLds &s, const Row &row, const Draw
     int before = s.flag;
     for (int i = 0; i < wave; ++i) before += s.part[i];
     if (d.j >= before && d.j < before + c) {  // one wave's share at most
-        for (int v = v0; v < v1; v += kWave) {
-            const uint32_t m = v + lane < v1 ? matches(row.vec()[v + lane]) : 0u;
+        for (int v = mine.v0; v < mine.v1; v += kWave) {
+            const uint32_t m = v + lane < mine.v1 ? equal.vec(row.vec()[v + lane]) : 0u;
             const int n = __popc(m), to = before + wave_incl_scan(n, lane);
             if (d.j >= to - n && d.j < to) {
                 uint32_t rest = m;
@@ -400,6 +488,37 @@ __device__ __forceinline__ int index_of(SampleLds &s, const Row &row, const Draw
             before = last_lane(to);
             if (before > d.j) break;
         }
+    }
+    __syncthreads();
+    return s.at;
+}
+
+// index_of among the row's entries of one half, up to kListed equals: all of
+// them are listed, and the one with j smaller indices is taken.
+template <bool kZero>
+__device__ __forceinline__ int index_in_half(SampleLds &s, const Row &row, bool second,
+                                             const Drawn &d) {
+    const int tid = threadIdx.x;
+    const Equal<kZero> equal(d.bits);
+    int *list = reinterpret_cast<int *>(s.narrow.bins);
+    auto found = [&](int i) {
+        const int slot = atomicAdd(&s.listed, 1);
+        if (slot < kListed) list[slot] = i;
+    };
+    if (tid < row.loose() && (tid >= row.head) == second && equal.one(row.p[row.loose_at(tid)]))
+        found(row.loose_at(tid));
+    for_vecs(row, second ? row.half() : 0, second ? row.vecs : row.half(), tid, kSampleThreads,
+             [&](u32x4 a, int v) {
+                 for (uint32_t m = equal.vec(a); m; m &= m - 1)
+                     found(row.head + 8 * v + __ffs((int)m) - 1);
+             });
+    __syncthreads();
+    const int n = s.listed < kListed ? s.listed : kListed;
+    for (int i = tid; i < n; i += kSampleThreads) {
+        const int x = list[i];
+        int before = 0;
+        for (int k = 0; k < n; ++k) before += list[k] < x;
+        if (before == d.j) s.at = x;
     }
     __syncthreads();
     return s.at;
@@ -421,11 +540,12 @@ __device__ __forceinline__ Drawn draw_wide(SampleLds &s, const Row &row, const D
     const uint32_t top = s.top;
     if (top == 0) return Drawn{0u, -1, 0};  // nothing to draw from
     const int first = 0xFFFF - (int)top;
-    if (!(d.T > 0.0) || d.k == 1) return Drawn{Wide::bits(first), 0, 2};
+    if (!(d.T > 0.0) || d.k == 1) return Drawn{Wide::bits(first), 0, 0};
     const double vmax = (double)bf16_f32((uint16_t)Wide::bits(first));
     auto weight = [&](int e) {
-        return e == first ? 1.0 : exp(((double)bf16_f32((uint16_t)Wide::bits(e)) - vmax) / d.T);
+        return e == first ? 1.0 : exp(((double)bf16_f32((uint16_t)Wide::bits(e)) - vmax) * d.per_T);
     };
+#pragma unroll 1
     for (int round = 0; round < 65536 / kWideRound; ++round) {
         for (int i = tid; i < kWideRound; i += kSampleThreads) h.bins[i] = 0;
         __syncthreads();
@@ -435,22 +555,23 @@ __device__ __forceinline__ Drawn draw_wide(SampleLds &s, const Row &row, const D
                 atomicAdd(&h.bins[e % kWideRound], 1u);
         });
         __syncthreads();
-        for (int i = wave; i < kWideRound / kWave; i += kSampleWaves)
-            sum_block(h, round * (kWideRound / kWave) + i, h.bins[i * kWave + lane], weight);
+#pragma unroll 1
+        for (int i = wave; i < kWideRound / kBlock; i += kSampleWaves)
+            sum_block(h, round * (kWideRound / kBlock) + i, h.bins + i * kBlock, weight);
         __syncthreads();
     }
     if (wave == 0) scan_blocks(h);
     __syncthreads();
     return walk_filters(h, d, weight, [&](int t) {
         __syncthreads();
-        if (tid < kWave) h.detail[tid] = 0;
+        if (tid < kBlock) h.detail[tid] = 0;
         __syncthreads();
         for_row(row, [&](uint32_t x) {
             const uint32_t key = value_key(x), e = 0xFFFFu - key;
-            if (key_counts(key) && (int)(e / kWave) == t) atomicAdd(&h.detail[e % kWave], 1u);
+            if (key_counts(key) && (int)(e / kBlock) == t) atomicAdd(&h.detail[e % kBlock], 1u);
         });
         __syncthreads();
-        return (int)h.detail[lane];
+        return reinterpret_cast<const u32x4 *>(h.detail)[lane];
     });
 }
 
@@ -471,25 +592,6 @@ __global__ __launch_bounds__(kSampleThreads, kSampleWavesPerSimd) void sample_ro
     if (r >= total) return;
     const bool exists = src >= 0 && src < cap;
     const Row row(p.logits + (int64_t)(exists ? src : 0) * p.V, exists ? p.V : 0);
-    for (int i = tid; i < kNarrowBlocks * kWave; i += kSampleThreads) h.bins[i] = 0;
-    if (tid == 0) {
-        s.top = kNarrowBlocks * kWave;
-        s.flag = 0;
-    }
-    __syncthreads();
-    {
-        char *bins = reinterpret_cast<char *>(h.bins);
-        auto count = [&](uint32_t off) { atomicAdd(reinterpret_cast<uint32_t *>(bins + off), 1u); };
-        for_vecs(row, 0, row.vecs, tid, kSampleThreads, [&](u32x4 a, int) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t two = narrow_offsets(a[i]);
-                count(two & 0xFFFFu);
-                count(two >> 16);
-            }
-        });
-        if (tid < row.loose()) count(narrow_offsets(row.p[row.loose_at(tid)]) & 0xFFFFu);
-    }
     const int b = wave_request_of(p.cu, p.B, r);
     Draw d;
     const bool owned = b < p.B && r >= p.cu[0];
@@ -498,12 +600,46 @@ __global__ __launch_bounds__(kSampleThreads, kSampleWavesPerSimd) void sample_ro
     d.top_p = owned && p.top_p ? (double)p.top_p[b] : 1.0;
     d.min_p = owned && p.min_p ? (double)p.min_p[b] : 0.0;
     d.u = p.uniforms[r] > 0.f ? (double)p.uniforms[r] : 0.0;
+    for (int i = tid; i < kNarrowBlocks * kBlock / 4; i += kSampleThreads)
+        reinterpret_cast<u32x4 *>(h.bins)[i] = u32x4{0u, 0u, 0u, 0u};
+    if (tid == 0) {
+        s.top = kNarrowBlocks * kBlock;
+        s.flag = 0;
+        s.listed = 0;
+        s.counted = 0;
+    }
+    __syncthreads();
+    {
+        char *bins = reinterpret_cast<char *>(h.bins);
+        const u16x2 end = narrow_end();
+        auto add = [&](uint32_t off, uint32_t one) {
+            atomicAdd(reinterpret_cast<uint32_t *>(bins + off), one);
+        };
+        auto count = [&](int v0, int v1, uint32_t one) {
+            for_vecs(row, v0, v1, tid, kSampleThreads, [&](u32x4 a, int) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t two = narrow_offsets(a[i], end);
+                    add(two & 0xFFFFu, one);
+                    add(two >> 16, one);
+                }
+            });
+        };
+        count(0, row.half(), kFirstHalf);
+        count(row.half(), row.vecs, kSecondHalf);
+        if (tid < row.loose())
+            add(narrow_offsets(row.p[row.loose_at(tid)], end) & 0xFFFFu,
+                tid < row.head ? kFirstHalf : kSecondHalf);
+    }
     __syncthreads();
 
-    const uint32_t high = h.bins[0], low = h.bins[kPlaceLow];
-    const uint32_t zeros = h.bins[kPlaceZero] + h.bins[kPlaceMinus];
-    if (zeros) {  // is it only zeros?
-        bool small = false;
+    d.per_T = 1.0 / d.T;
+    const bool high = __ballot(h.bins[lane] != 0) != 0;
+    const int low = last_lane(wave_incl_scan(Narrow::count(h.bins[kPlaceLow + lane]), lane));
+    const uint32_t z0 = h.bins[kPlaceZero], z1 = h.bins[kPlaceMinus];
+    const uint32_t zeros[2] = {(z0 & 0xFFFFu) + (z1 & 0xFFFFu), (z0 >> 16) + (z1 >> 16)};
+    if (zeros[0] | zeros[1]) {  // is it only zeros, and do they fit?
+        bool small = (zeros[0] | zeros[1]) > 0xFFFFu;
         for_row(row, [&](uint32_t x) {
             const uint32_t m = x & 0x7FFFu;
             small |= m > 0 && m < kNarrowLo;
@@ -511,48 +647,73 @@ __global__ __launch_bounds__(kSampleThreads, kSampleWavesPerSimd) void sample_ro
         if (small) s.flag = 1;
     }
     __syncthreads();
+    if (wave == 0) h.bins[kPlaceLow + lane] = 0;
     if (tid == 0) {
-        h.bins[kPlaceZero] = zeros;
+        h.bins[kPlaceZero] = zeros[0] | zeros[1] << 16;
         h.bins[kPlaceMinus] = 0;
-        h.bins[kPlaceLow] = 0;
     }
     __syncthreads();
+    int sum = 0;
+    bool empty = true;
+#pragma unroll 1
     for (int i = wave; i < kNarrowBlocks; i += kSampleWaves) {
-        const uint64_t m = __ballot(h.bins[i * kWave + lane] != 0);
-        if (m) {
-            if (lane == 0) atomicMin(&s.top, (unsigned)(i * kWave + __ffsll((unsigned long long)m) - 1));
-            break;
-        }
+        const u32x4 n = reinterpret_cast<const u32x4 *>(h.bins + i * kBlock)[lane];
+        const uint64_t m = __ballot((n[0] | n[1] | n[2] | n[3]) != 0);
+        if (m == 0) continue;
+        if (empty && lane == __ffsll((unsigned long long)m) - 1)
+            atomicMin(&s.top, (unsigned)(i * kBlock + kPer * lane +
+                                         (n[0] ? 0 : n[1] ? 1 : n[2] ? 2 : 3)));
+        empty = false;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) sum += Narrow::count(n[u]);
     }
+    sum = last_lane(wave_incl_scan(sum, lane));
+    if (lane == 0) atomicAdd(&s.counted, sum);
     __syncthreads();
     const int top = (int)s.top;
     const bool small = s.flag != 0;
     const bool greedy = !(d.T > 0.0) || d.k == 1;
     const double vmax = (double)bf16_f32((uint16_t)Narrow::bits(top));
-    const bool narrow = high == 0 && !small && top < kPlaceLow &&
-                        (low == 0 || greedy || (vmax + 65536.0) / d.T > kNegligible);
+    const bool narrow = !high && !small && top < kPlaceLow && s.counted + low == row.V &&
+                  (low == 0 || greedy || (vmax + 65536.0) * d.per_T > kNegligible);
     Drawn out;
-    if (!exists) {
-        out = Drawn{0u, -2, 0};
-    } else if (!narrow) {
-        __syncthreads();
-        out = draw_wide(s, row, d);
-    } else if (greedy) {
-        out = Drawn{Narrow::bits(top), 0, (int)h.bins[top]};
-    } else {
+    if (narrow && greedy) {
+        out = Drawn{Narrow::bits(top), 0, top};
+    } else if (narrow) {
         auto weight = [&](int e) {
-            return e == top ? 1.0 : exp(((double)bf16_f32((uint16_t)Narrow::bits(e)) - vmax) / d.T);
+            return exp(((double)bf16_f32((uint16_t)Narrow::bits(e)) - vmax) * d.per_T);
         };
+#pragma unroll 1
         for (int i = wave; i < kNarrowBlocks; i += kSampleWaves)
-            sum_block(h, i, h.bins[i * kWave + lane], weight);
+            sum_block(h, i, h.bins + i * kBlock, weight);
         __syncthreads();
         if (wave == 0) scan_blocks(h);
         __syncthreads();
-        out = walk_filters(h, d, weight, [&](int t) { return (int)h.bins[t * kWave + lane]; });
+        out = walk_filters(h, d, weight, [&](int t) {
+            return reinterpret_cast<const u32x4 *>(h.bins + t * kBlock)[lane];
+        });
     }
-    __syncthreads();
-    // nothing to draw from: the lowest index; no such source row: -1
-    const int chosen = out.j < 0 ? out.j + 1 : index_of(s, row, out);
+    int chosen = -1;
+    if (exists && narrow) {
+        const uint32_t c = h.bins[out.place];
+        const int ahead = (int)(c & 0xFFFFu), all = Narrow::count(c);
+        const bool second = out.j >= ahead;
+        __syncthreads();
+        if ((second ? all - ahead : ahead) <= kListed) {
+            Drawn in = out;
+            in.j -= second ? ahead : 0;
+            chosen = out.bits ? index_in_half<false>(s, row, second, in)
+                              : index_in_half<true>(s, row, second, in);
+        } else {
+            chosen = out.bits ? index_of<false>(s, row, out) : index_of<true>(s, row, out);
+        }
+    } else if (exists) {
+        __syncthreads();
+        out = draw_wide(s, row, d);
+        // nothing to draw from: the lowest index
+        if (out.j < 0) chosen = 0;
+        else chosen = out.bits ? index_of<false>(s, row, out) : index_of<true>(s, row, out);
+    }
     if (!owned) return;
     if (!arrivals) {
         if (tid == 0) p.sample[r] = chosen;

@@ -253,3 +253,61 @@ def test_graph_replays_match_eager():
         eager = call(c)
         for g, w in zip((out["packed_sample"], out["accepted"], out["bonus"]), eager):
             assert torch.equal(g, w)
+
+
+def fill(c, value, where):
+    c["logits"] = torch.where(where, torch.tensor(value).bfloat16(), c["logits"])
+
+
+@pytest.mark.parametrize("V", [140001, 262147])
+@pytest.mark.parametrize("greedy", [False, True])
+def test_more_equals_than_16_bits_count(V, greedy):
+    """One value 65536 times and more in either half of a row, or in one of them."""
+    for lo, hi in ((0, V), (0, 65536), (V - 65536, V), (3, 65535 + 3), (V // 2, V)):
+        c = make(2, 1, V, seed=50, filters="none")
+        if greedy:
+            c["temperature"][:] = 0.0
+        at = torch.arange(V)
+        fill(c, 20.0, ((at >= lo) & (at < hi))[None].expand(c["logits"].shape))
+        check(c)
+
+
+@pytest.mark.parametrize("V", [4099, 150001])
+def test_more_equals_than_are_listed(V):
+    """A drawn value with over a thousand equals, whose order decides."""
+    c = make(20, 2, V, seed=51, filters="none")
+    c["logits"] = (torch.round(c["logits"].float() / 2) * 2).bfloat16()
+    check(c)
+
+
+@pytest.mark.parametrize("value", [65280.0, 65536.0, -65536.0, 2.0 ** -32, -2.0 ** -33, 2.0 ** -40,
+                                   float("inf"), float("nan")])
+@pytest.mark.parametrize("T", [0.0, 1.0, 3000.0])
+def test_values_at_the_ends_of_the_counted_range(value, T):
+    c = make(9, 2, 3001, seed=52, filters="mixed")
+    c["temperature"][:] = T
+    at = torch.rand(c["logits"].shape, generator=torch.Generator().manual_seed(3)) < 0.01
+    at[::3] = False
+    fill(c, value, at)
+    check(c)
+    c["logits"] = -c["logits"]
+    check(c)
+
+
+@pytest.mark.parametrize("V", [1, 3, 9, 15, 23, 1003])
+@pytest.mark.parametrize("T", [0.0, 1.0])
+def test_the_last_entries_of_rows_at_every_alignment(V, T):
+    c = make(16, 1, V, seed=53, filters="none")
+    c["temperature"][:] = T
+    for i in range(c["logits"].shape[0]):
+        c["logits"][i, V - 1 - i % min(V, 9)] = 30.0
+    check(c)
+
+
+def test_a_masked_vocabulary_over_16_bits():
+    for mask in (float("-inf"), -3.3895313892515355e38, -1e9):
+        c = make(3, 2, 200003, seed=54)
+        keep = torch.rand(c["logits"].shape, generator=torch.Generator().manual_seed(4)) < 1e-4
+        keep[:, 5] = True
+        fill(c, mask, ~keep)
+        check(c)
