@@ -136,6 +136,7 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTileKeys = 64;
 constexpr int kBlockRows = 128;
@@ -251,7 +252,9 @@ struct Tiles {
         };
         uint64_t before[kGroupRequests + 1];
         uint64_t part[kTileWaves];
-        int holes[2][kTileWaves];  // rows without a page, a bit per row of a wave's 16
+        // a bit per row of a wave's 16: those without a page, and in the upper
+        // half those whose values were not all finite
+        uint32_t marks[2][kTileWaves];
         int last;
     };
 
@@ -262,6 +265,7 @@ struct Tiles {
         int lo, hi;         // positions that exist for the block
         int ctx, pos;       // of the request; of this lane's query row
         int pos_min, pos_max;  // over the wave's query rows
+        int first, final;      // over the block's
         bool active;
         float c;            // scores to powers of two
     };
@@ -337,25 +341,91 @@ struct Tiles {
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false)),
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true))};
     }
-    __device__ static __forceinline__ void put(char *buf, int r, int lane, u32x4 x) {
+    __device__ static __forceinline__ void put(char *buf, int r, int lane, u32x4 x, bool scrub,
+                                               bool &bad) {
         const int f = swizzle<D>(r), c = lane % kRowLanes;
         char *row = buf + r * (D * 2);
         if (kE4m3) {  // 16 values are two chunks of bf16, exactly
-            *reinterpret_cast<u32x4 *>(row + (((2 * c) ^ f) << 4)) = widen(x[0], x[1]);
-            *reinterpret_cast<u32x4 *>(row + (((2 * c + 1) ^ f) << 4)) = widen(x[2], x[3]);
+            u32x4 y = widen(x[0], x[1]), z = widen(x[2], x[3]);
+            if (scrub) bad = scrubbed(y) | scrubbed(z);
+            *reinterpret_cast<u32x4 *>(row + (((2 * c) ^ f) << 4)) = y;
+            *reinterpret_cast<u32x4 *>(row + (((2 * c + 1) ^ f) << 4)) = z;
         } else {
+            if (scrub) bad = scrubbed(x);
             *reinterpret_cast<u32x4 *>(row + ((c ^ f) << 4)) = x;
         }
     }
-    __device__ static __forceinline__ void store(Lds &s, int buf, const Regs &g) {
+    // Sets what is not finite to 0; whether anything was.
+    __device__ static __forceinline__ bool scrubbed(u32x4 &x) {
+        u16x2 top = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[i] & 0x7F807F80u));
+        const bool bad = top[0] == 0x7F80 || top[1] == 0x7F80;
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((x[i] & 0x7F80u) == 0x7F80u) x[i] &= 0xFFFF0000u;
+                if ((x[i] & 0x7F800000u) == 0x7F800000u) x[i] &= 0xFFFFu;
+            }
+        }
+        return bad;
+    }
+    // Whether some row of the block does not see some key of the tile that another
+    // one sees. There a weight of zero must keep out whatever the value is, which
+    // zero times an infinity or NaN would not: values that are not finite are
+    // staged as 0, and add_bad adds them to the rows that see them.
+    __device__ static __forceinline__ bool partial(const AttendParams &p, const Task &t, int tile) {
+        const int k0 = tile * kTileKeys;
+        return k0 + kTileKeys - 1 > t.first || (p.window > 0 && k0 <= t.final - p.window);
+    }
+    __device__ static __forceinline__ void store(Lds &s, int buf, const Regs &g, bool scrub) {
         const int lane = threadIdx.x & (kWave - 1);
+        uint32_t marks = (uint32_t)g.holes;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int r = wave_id() * 16 + i * kLoadRows + lane / kRowLanes;
-            put(s.stage[buf][0], r, lane, g.k[i]);
-            put(s.stage[buf][1], r, lane, g.v[i]);
+            bool bad = false;
+            put(s.stage[buf][0], r, lane, g.k[i], false, bad);
+            put(s.stage[buf][1], r, lane, g.v[i], scrub, bad);
+            const uint64_t m = __ballot(bad);
+            if (m) {
+#pragma unroll
+                for (int x = 0; x < kLoadRows; ++x)
+                    marks |= (m >> (x * kRowLanes) & ((1ull << kRowLanes) - 1))
+                                 ? 0x10000u << (i * kLoadRows + x) : 0u;
+            }
         }
-        if (lane == 0) s.holes[buf][wave_id()] = g.holes;
+        if (lane == 0) s.marks[buf][wave_id()] = marks;
+    }
+
+    // The values that `store` left out, from the cache again: to the rows that
+    // see them. Their weights do not matter: the sum is not finite with any.
+    __device__ static __forceinline__ void add_bad(const uint32_t *marks, int tile, int sub,
+                                                   int keys, const AttendParams &p, const Task &t,
+                                                   State &st) {
+        const int h = (threadIdx.x >> 5) & 1;
+#pragma unroll 1
+        for (int y = sub * 32; y < sub * 32 + keys; ++y) {
+            if (!(marks[y / 16] >> (16 + y % 16) & 1)) continue;
+            const int key = tile * kTileKeys + y, pg = page_of(p.c, key);
+            const int64_t at = (int64_t)t.table[pg] * p.c.page_stride + t.head_off +
+                               (int64_t)(key - pg * p.c.page) * p.c.slot_stride;
+            const bool see = visible(p, t, key);
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float v = load1<kE4m3>(p.c.v, at + d * 32 + 8 * (r / 4) + 4 * h + (r & 3));
+                    st.o[d][r] += see && !(fabsf(v) < INFINITY) ? v : 0.f;
+                    __builtin_amdgcn_sched_barrier(0);  // one at a time: registers, not speed
+                }
+        }
+    }
+    // Whether this lane's query row sees a position that has a page.
+    __device__ static __forceinline__ bool visible(const AttendParams &p, const Task &t, int key) {
+        return key <= t.pos && key >= t.lo && key < t.hi &&
+               (p.window == 0 || key > t.pos - p.window);
     }
 
     // One staged tile against the wave's 32 query rows: kSub subtiles of 32
@@ -367,12 +437,12 @@ struct Tiles {
         const int lane = threadIdx.x & (kWave - 1);
         const int h = lane >> 5;
         const int k0 = tile * kTileKeys + sub * 32, k1 = k0 + kSub * 32 - 1;
-        const int32_t *ho = s.holes[buf];
-        const int hole = __builtin_amdgcn_readfirstlane(ho[0] | ho[1] | ho[2] | ho[3]);
+        const uint32_t *ho = s.marks[buf];
+        const uint32_t marks = __builtin_amdgcn_readfirstlane(ho[0] | ho[1] | ho[2] | ho[3]);
         if (k0 > t.pos_max || k0 >= t.hi || k1 < t.lo ||
             (p.window > 0 && k1 <= t.pos_min - p.window))
             return;
-        const bool whole = k1 <= t.pos_min && k1 < t.hi && k0 >= t.lo && hole == 0 &&
+        const bool whole = k1 <= t.pos_min && k1 < t.hi && k0 >= t.lo && marks == 0 &&
                            (p.window == 0 || k0 > t.pos_max - p.window);
         const char *kb = s.stage[buf][0] + sub * 32 * D * 2;
         const char *vb = s.stage[buf][1] + sub * 32 * D * 2;
@@ -400,15 +470,12 @@ struct Tiles {
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
                 const int w = (sub + i) * 2;
-                const uint32_t no = (uint32_t)(ho[w] & 0xFFFF) | ((uint32_t)ho[w + 1] << 16);
+                const uint32_t no = (ho[w] & 0xFFFFu) | (ho[w + 1] << 16);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int y = 8 * (r / 4) + 4 * h + (r & 3);
                     const int key = k0 + i * 32 + y;
-                    const bool see = key <= t.pos && key >= t.lo && key < t.hi &&
-                                     (p.window == 0 || key > t.pos - p.window) &&
-                                     !(no >> y & 1);
-                    x[i][r] = see ? x[i][r] : -INFINITY;
+                    x[i][r] = visible(p, t, key) && !(no >> y & 1) ? x[i][r] : -INFINITY;
                 }
             }
         }
@@ -469,6 +536,7 @@ struct Tiles {
                 }
             }
         }
+        if (marks >> 16) add_bad(ho, tile, sub, kSub * 32, p, t, st);
     }
 
     template <int kSub>
@@ -479,7 +547,7 @@ struct Tiles {
         lookup(p.c, t, tile, e);
         load(p.c, t, tile, e, g);
         if (n > 1) lookup(p.c, t, tile + 1, e);
-        store(s, 0, g);
+        store(s, 0, g, partial(p, t, tile));
         for (int i = 0; i < n; ++i) {
             if (i + 1 < n) {
                 load(p.c, t, tile + i + 1, e, g);
@@ -488,7 +556,7 @@ struct Tiles {
             __syncthreads();
             if (t.active) compute<kSub>(s, i & 1, tile + i, sub, p, t, st);
             // the other buffer's readers passed the barrier above
-            if (i + 1 < n) store(s, (i + 1) & 1, g);
+            if (i + 1 < n) store(s, (i + 1) & 1, g, partial(p, t, tile + i + 1));
         }
         __syncthreads();
     }
@@ -616,6 +684,8 @@ __global__ __launch_bounds__(kTileThreads, kTileWgsPerCu) void attend_tile_kerne
         t.hi = k.hi;
         t.ctx = q.ctx;
         t.pos = q.ctx + j;
+        t.first = q.ctx + m0 / G;
+        t.final = q.ctx + (m0 + rows - 1) / G;
         t.pos_min = q.ctx + (m0 + qt * 32) / G;
         const int m_last = (qt * 32 + 31 < rows - 1 ? qt * 32 + 31 : rows - 1) + m0;
         t.pos_max = q.ctx + m_last / G;

@@ -230,3 +230,46 @@ def test_graph_replays_with_new_lengths():
         want, tol = ref.attend(c["q"], c["kc"], c["vc"], starts, lens, c["table"], 17,
                                out=torch.full(out.shape, 7.0).bfloat16())
         assert bool(((got.cpu().double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("rows,ctx", [([4], [61]), ([17, 1, 9], [300, 63, 5]), ([70, 33], [0, 40])])
+@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_infinities_that_only_later_rows_see(rows, ctx, D, cache):
+    """Values (and keys) that are not finite at a position change no row before
+    it, though the rows share its tile; the rows that see it are not finite."""
+    c = make(rows, ctx, 4, 2, D, 16, cache, seed=12)
+    clean = check(c, **SCALES[cache])
+    bad = float("nan") if cache == "e4m3" else float("inf")
+    # the position of every request's second-to-last row
+    hit = [(b, c["ctx"][b] + n - 2) for b, n in enumerate(rows) if n > 1]
+    for pool in ("vc", "kc"):
+        x = dict(c, kc=c["kc"].clone(), vc=c["vc"].clone())
+        for b, t in hit:
+            page = x[pool][int(c["table"][b, t // 16])].float()
+            page[:, t % 16, 3::7] = bad if pool == "vc" else float("nan")
+            raw = page.to(x[pool].dtype).view(torch.uint8)
+            x[pool].view(torch.uint8)[int(c["table"][b, t // 16])] = raw
+        out = torch.zeros((c["cap"], c["Hq"], D), dtype=torch.bfloat16, device=DEV)
+        got = call(x, *pools(x, DEV), out, **SCALES[cache]).cpu().double()
+        for b, n in enumerate(rows):
+            r0, sees = c["cu"][b], 2 if n > 1 else 0
+            assert torch.equal(got[r0:r0 + n - sees], clean[r0:r0 + n - sees])
+            if sees:
+                assert not bool(got[r0 + n - 2:r0 + n, :, 3::7].isfinite().any())
+
+
+@pytest.mark.parametrize("D", [64, 128, 96])
+def test_infinities_that_a_window_has_left_behind(D):
+    c = make([17, 80], [100, 0], 4, 2, D, 16, seed=13)
+    kw = dict(window=20)
+    clean = check(c, **kw)
+    # seen by each request's first rows only
+    for b, t, first in ((0, 95, 15), (1, 3, 23)):
+        c["vc"][int(c["table"][b, t // 16]), :, t % 16] = float("-inf")
+        kc, vc = pools(c, DEV)
+        out = torch.zeros((c["cap"], c["Hq"], D), dtype=torch.bfloat16, device=DEV)
+        got = call(c, kc, vc, out, **kw).cpu().double()
+        r0, n = c["cu"][b], c["cu"][b + 1] - c["cu"][b]
+        assert torch.equal(got[r0 + first:r0 + n], clean[r0 + first:r0 + n])
+        assert not bool(got[r0 + (0 if b == 0 else 3):r0 + first].isfinite().any())
