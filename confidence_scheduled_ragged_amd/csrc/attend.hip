@@ -7,6 +7,8 @@
 //   O = sum_t exp(x_t - m) V_t / sum_t exp(x_t - m),  x_t = scale (q . K_t),
 // with m the largest x_t. A running maximum and sum carry the softmax over the
 // keys in one pass; a row that sees nothing gives zeros.
+#include <type_traits>
+
 #include "forward.hpp"
 
 namespace dspark {
@@ -116,19 +118,27 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
 // ---------------------------------------------------------------- tiled kernel
 //
 // Rows of one key-value head share its keys: with G query heads per key-value
-// head, a request's n rows are M = n*G query rows, taken in blocks of up to 128
-// against tiles of 64 positions. A (head, block) is a unit; the tiles of all units,
-// laid end to end, are divided evenly between the resident workgroups, so any
-// mix of long and short requests fills the chip, a single long context
-// included, and no launch shape depends on the lengths. A unit that ends up in
-// several workgroups leaves partial results (maximum, sum, weighted values) in
-// the workspace, and the last workgroup to arrive joins them in tile order.
+// head, a request's n rows are M = n*G query rows, taken in blocks of up to 256
+// against tiles of 64 to 256 positions (32 KiB of keys and values). A (head,
+// block) is a unit; the tiles of all units, laid end to end, are divided evenly
+// between the resident workgroups, so any mix of long and short requests fills
+// the chip, a single long context included, and no launch shape depends on the
+// lengths. A unit that ends up in several workgroups leaves partial results
+// (maximum, sum, weighted values) in the workspace, and the last workgroup to
+// arrive joins them in tile order.
+//
+// One workgroup of eight waves a CU holds four tiles in LDS: one in use, three
+// on their way, loaded straight into LDS without passing registers, whatever
+// unit they belong to. Ordinary batches are bound by HBM, and 96 KiB a CU in
+// flight is what keeps it busy: with one tile ahead, through registers, and two
+// workgroups a CU the loads alone took 326 of the 409 us of the mixed batch.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds 16 of a query's 32
 // scores of one MFMA (the other 16 sit in lane ^ 32), so the softmax needs one
 // exchange between the halves, and the weights leave the exponential in the
 // very places where the next product, O^T = V^T P^T, wants them. V^T comes
-// from row-major V in LDS through the transposing LDS reads.
+// from row-major V in LDS through the transposing LDS reads. 8-bit tiles stay as
+// they are in LDS and are widened, exactly, on their way to the matrix product.
 //
 // Weights are rounded to bf16 before their product with V (half a step 2^-8 of
 // each weight, averaged over the keys); sums, maxima and outputs stay in fp32.
@@ -137,59 +147,81 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kTileKeys = 64;
-constexpr int kBlockRows = 128;
-constexpr int kTileThreads = 256;
-constexpr int kTileWaves = kTileThreads / kWave;
-constexpr int kTileWgsPerCu = 2;
-constexpr int kGroupRequests = 1024;  // of one launch; larger batches take several
+constexpr int kNarrowRows = 128, kWideRows = 256;  // query rows of a block
+constexpr int kSlotBytes = 32768;                  // of a tile in LDS: keys, then values
+constexpr int kHalfSlot = kSlotBytes / 2;
+constexpr int kGroupRequests = 512;  // of one launch; larger batches take several
 constexpr int kMinTiles = 2;          // per workgroup: fewer would cost more to join than to read
+constexpr int kZeroBytes = 256;       // of the workspace that stay zero
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct TileParams {
     AttendParams a;
+    const char *zeros;   // kZeroBytes
     unsigned *arrivals;  // [wgs], zero between calls
     float *slots;        // [2 * wgs] partial results of slot_rows rows
     int slot_rows;
+    // 16 slots in a row share a page, and a page and 16 slots are below 2^32 bytes
+    bool together;
+    uint32_t page_bytes, slot_bytes;
 };
 
 // Floats of one partial result: (maximum, sum) and D values of each row.
 __host__ __device__ inline int64_t slot_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
 
+// The lengths and the table are read by scalar loads, apart from the loads into
+// LDS, which return in order.
+typedef const __attribute__((address_space(4))) int32_t *ScalarInts;
+__device__ __forceinline__ int scalar_load(const int32_t *p, int64_t i) {
+    return ((ScalarInts)(uintptr_t)p)[i];
+}
+
 struct Request {
     int start, ctx, M, blocks;
 };
-__device__ __forceinline__ Request load_request(const AttendParams &p, int b) {
+template <int kBlockRows>
+__device__ __forceinline__ Request request_of(const AttendParams &p, int s, int e, int c) {
     Request q;
-    int s = p.cu[b], e = p.cu[b + 1];
     s = s < 0 ? 0 : (s > p.rows ? p.rows : s);
     e = e < s ? s : (e > p.rows ? p.rows : e);
     const int n = e - s < p.max_rows ? e - s : p.max_rows;
-    const int c = p.ctx[b];
     q.start = s;
     q.ctx = c < 0 ? 0 : (c > (1 << 30) ? 1 << 30 : c);
     q.M = n * (p.Hq / p.Hkv);
     q.blocks = (q.M + kBlockRows - 1) / kBlockRows;
     return q;
 }
-// Positions [lo, hi) that block i of a request needs, and its tiles (one at
-// least: a block that sees nothing still writes its zeros).
+template <int kBlockRows>
+__device__ __forceinline__ Request load_request(const AttendParams &p, int b) {
+    return request_of<kBlockRows>(p, p.cu[b], p.cu[b + 1], p.ctx[b]);
+}
+template <int kBlockRows>
+__device__ __forceinline__ Request scalar_request(const AttendParams &p, int b) {
+    return request_of<kBlockRows>(p, scalar_load(p.cu, b), scalar_load(p.cu, b + 1), scalar_load(p.ctx, b));
+}
+// Positions [lo, hi) that block i of a request needs, its first and last row's
+// positions, and its tiles (one at least: a block that sees nothing still writes
+// its zeros).
 struct Block {
-    int lo, hi, tile, tiles;
+    int lo, hi, first, final, tile, tiles;
 };
+template <int kBlockRows, int kKeys>
 __device__ __forceinline__ Block block_of(const AttendParams &p, const Request &q, int i) {
     const int G = p.Hq / p.Hkv;
     const int m0 = i * kBlockRows;
     const int m1 = (q.M < m0 + kBlockRows ? q.M : m0 + kBlockRows) - 1;
     const int64_t width = (int64_t)p.c.table_width * p.c.page;
     Block k;
+    k.first = q.ctx + m0 / G;
+    k.final = q.ctx + m1 / G;
     k.lo = 0;
-    if (p.window > 0 && q.ctx + m0 / G + 1 > p.window) k.lo = q.ctx + m0 / G + 1 - p.window;
-    const int end = q.ctx + m1 / G + 1;
+    if (p.window > 0 && k.first + 1 > p.window) k.lo = k.first + 1 - p.window;
+    const int end = k.final + 1;
     k.hi = end < width ? end : (int)width;
-    k.tile = k.lo / kTileKeys;
-    const int last = (k.hi + kTileKeys - 1) / kTileKeys;
+    k.tile = k.lo / kKeys;
+    const int last = (int)(((int64_t)k.hi + kKeys - 1) / kKeys);
     k.tiles = last > k.tile ? last - k.tile : 1;
     return k;
 }
@@ -227,255 +259,443 @@ __device__ __forceinline__ f32x2 load_coherent(const float *p) {
     return f32x2{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
 }
 
-// Chunk (16 bytes) c of row r of a staged tile sits at chunk c ^ swizzle(r): 16
-// neighbouring rows then lie in different banks for the score operand (one
-// chunk of 32 rows), and 4 rows in different quarters of the banks for the
-// transposed reads (4 chunks of 8 rows).
-template <int D>
-__device__ __forceinline__ int swizzle(int r) {
-    if (D >= 128) return ((r & 3) << 2) | ((r >> 2) & 3);
-    return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+// Waits until at most kLoads of this wave's vector loads are on their way and its
+// LDS accesses are done.
+template <int kLoads>
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((kLoads & 15) | (7 << 4) | ((kLoads >> 4) << 14));
 }
 
+// Chunk (16 bytes) c of row r of a staged tile sits at chunk c ^ swizzle(r), so
+// that the score operand (one chunk of 32 rows) and the transposed reads (8 or
+// 16 rows of two to four chunks) each meet few equal banks.
 template <int D, bool kE4m3>
+__device__ __forceinline__ int swizzle(int r) {
+    if (!kE4m3 && D == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+    if (!kE4m3) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    if (D == 128) return ((r >> 2) & 1) | (r & 2) | (((r >> 3) & 1) << 2);
+    return (r >> 2) & 3;
+}
+
+template <int D, bool kE4m3, bool kWide>
 struct Tiles {
+    static constexpr int kWaves = kWide ? 8 : 4;
+    static constexpr int kThreads = kWaves * kWave;
+    static constexpr int kSlots = kWide ? 4 : 2;         // tiles in LDS
+    static constexpr int kBlockRows = kWide ? kWideRows : kNarrowRows;
     static constexpr int kItem = kE4m3 ? 1 : 2;
-    static constexpr int kRowLanes = D * kItem / 16;       // lanes of 16 bytes per row
-    static constexpr int kLoadRows = kWave / kRowLanes;    // rows of one wave's load
-    static constexpr int kLoads = 16 / kLoadRows;          // a wave stages 16 rows of a tile
-    static constexpr int kTileBytes = kTileKeys * D * 2;   // of K or V in LDS, as bf16
+    static constexpr int kRow = D * kItem;               // bytes
+    static constexpr int kChunks = kRow / 16;            // of a row
+    static constexpr int kKeys = kHalfSlot / kRow;       // positions of a tile
+    static constexpr int kLoadRows = kWave / kChunks;    // rows of one load (4, 8 or 16)
+    static constexpr int kStagers = kWaves / 2;          // waves that stage keys, and values
+    static constexpr int kWaveRows = kKeys / kStagers;   // rows that each of them stages
+    static constexpr int kWaveLoads = kHalfSlot / kStagers / 1024;  // of 1 KiB
+    static constexpr int kEntries = kWaveRows / 16;      // 16 rows each
 
     struct Lds {
-        union {
-            char stage[2][2][kTileBytes];  // [buffer][K, V]
-            float join[2][(D / 2 + 2) * kWave];
-        };
         uint64_t before[kGroupRequests + 1];
-        uint64_t part[kTileWaves];
-        // a bit per row of a wave's 16: those without a page, and in the upper
-        // half those whose values were not all finite
-        uint32_t marks[2][kTileWaves];
+        uint64_t part[kWaves];
+        float join[16 * (kWaves / 2) * kWave];
+        f32x2 ml[kWaves / 2 * kWave];
+        uint64_t bad[kSlots][kStagers];  // rows whose values were not all finite, per staging wave
         int last;
     };
 
-    // What one wave works on inside a unit.
+    // The tiles in LDS are variables of their own, not one array: the compiler
+    // then knows which loads into LDS a read of keys has to wait for, where the slot
+    // is chosen by a branch.
+    struct Slots {
+        char *at0, *at1, *at2, *at3;
+        template <typename F>
+        __device__ __forceinline__ void pick(int n, F f) const {
+            if (kSlots == 2 || n < 2) {
+                if (n == 0) f(at0);
+                else f(at1);
+            } else if (n == 2) {
+                f(at2);
+            } else {
+                f(at3);
+            }
+        }
+        __device__ static __forceinline__ uint32_t address(const char *p) {
+            uint32_t a = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p;
+            asm("" : "+s"(a));  // or the choice becomes a table, which LDS addresses cannot fill
+            return a;
+        }
+        __device__ __forceinline__ uint32_t address(int n) const {
+            return kSlots == 2 || n < 2 ? (n == 0 ? address(at0) : address(at1))
+                                        : (n == 2 ? address(at2) : address(at3));
+        }
+    };
+
+    // A unit, and the tiles of it from `tile` on that are this workgroup's.
+    struct Unit {
+        int b, head, blk;
+        Request q;
+        Block k;
+        int tile, left;  // next tile; tiles left in the unit
+    };
+    // The wave's part of a unit.
     struct Task {
         const int32_t *table;
-        int64_t head_off;   // of the key-value head in the pools
-        int lo, hi;         // positions that exist for the block
-        int ctx, pos;       // of the request; of this lane's query row
+        int64_t head_off;      // of the key-value head in the pools
+        int lo, hi, first, final;
+        int pos;               // of this lane's query row
         int pos_min, pos_max;  // over the wave's query rows
-        int first, final;      // over the block's
-        bool active;
-        float c;            // scores to powers of two
+        bool active, hole;     // hole: some position may have no page
+        float c;               // scores to powers of two
     };
     struct State {
         bf16x8 q[D / 16];
         f32x16 o[D / 32];
         float m, l;
     };
-    struct Regs {
-        u32x4 k[kLoads], v[kLoads];
-        int holes;
-    };
-    struct Entry {
-        int at[kLoads];
-    };
 
     __device__ static __forceinline__ int wave_id() {
         return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     }
+    __device__ static __forceinline__ bool named(const PagedCache &c, int at) {
+        return at >= 0 && at < c.pages;
+    }
 
-    // Table entries of the rows that this lane loads of a tile (-1: no page).
-    // Pages of a multiple of 16 slots hold a wave's 16 rows together.
-    __device__ static __forceinline__ void lookup(const PagedCache &c, const Task &t, int tile,
-                                                  Entry &e) {
+    // ------------------------------------------------------------- staging
+    struct Stager {
+        const char *base;          // the unit's head in the pool of keys or values
+        const int32_t *table;      // the unit's pages
+        int row0;                  // of the wave's rows in a tile
+        uint32_t off[kWaveLoads];  // this lane's bytes from the first of 16 rows
+        // pages of the wave's rows, 16 each, in tiles batch0 + lane: one load for 64
+        // tiles, since a wait for it waits for the tiles on their way too
+        int batch[kEntries];
+        int batch0;
+    };
+    __device__ static __forceinline__ void stager(const TileParams &tp, Stager &g) {
+        const PagedCache &c = tp.a.c;
+        const int lane = threadIdx.x & (kWave - 1), w = wave_id();
+        g.row0 = w % kStagers * kWaveRows;
+#pragma unroll
+        for (int j = 0; j < kWaveLoads; ++j) {
+            const int r = j * kLoadRows + lane / kChunks;
+            g.off[j] = (uint32_t)(r % 16) * tp.slot_bytes +
+                       (((lane % kChunks) ^ swizzle<D, kE4m3>(r)) << 4);
+        }
+    }
+    __device__ static __forceinline__ void enter(const TileParams &tp, Stager &g, const Unit &u) {
+        const PagedCache &c = tp.a.c;
+        g.base = static_cast<const char *>(wave_id() < kStagers ? c.k : c.v) +
+                 (int64_t)u.head * c.head_stride * kItem;
+        g.table = c.table + (int64_t)u.b * c.table_width;
+    }
+    __device__ static __forceinline__ void look_up(const TileParams &tp, Stager &g, int tile) {
+        const PagedCache &c = tp.a.c;
         const int lane = threadIdx.x & (kWave - 1);
-        const int first = tile * kTileKeys + wave_id() * 16;
-        if (c.page % 16 == 0) {
-            const int pg = page_of(c, first);
-            e.at[0] = pg < c.table_width ? t.table[pg] : -1;
+        g.batch0 = tile;
+        if (!tp.together) return;
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) {
+            const int64_t pos = (int64_t)(tile + lane) * kKeys + g.row0 + 16 * e;
+            const int pg = pos > 0x7FFFFFFF ? c.table_width : page_of(c, (int)pos);
+            g.batch[e] = pg < c.table_width ? g.table[pg] : -1;
+        }
+    }
+    __device__ static __forceinline__ void dma(const char *from, char *to) {
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void *)from,
+            (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+    }
+    // The wave's loads of one tile into a slot. Rows without a page come from the
+    // zeros. Rows of a page that lie outside [lo, hi) are loaded as they are: they
+    // are masked like rows that a query does not see.
+    __device__ static __forceinline__ void issue(const TileParams &tp, const Stager &g, int tile,
+                                                 const Slots &slots, int number, int lane) {
+        const PagedCache &c = tp.a.c;
+        const int w = wave_id();
+        const char *from[kWaveLoads];
+        if (tp.together) {
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) {
+                const int at = __builtin_amdgcn_readlane(g.batch[e], tile - g.batch0);
+                const bool ok = (unsigned)at < (unsigned)c.pages;
+                const int pos = tile * kKeys + g.row0 + 16 * e;
+                const uint32_t slot = (uint32_t)(pos - page_of(c, pos) * c.page);
+                const char *base = ok ? g.base + (uint64_t)(uint32_t)at * tp.page_bytes +
+                                            slot * tp.slot_bytes
+                                      : tp.zeros;
+#pragma unroll
+                for (int j = e * kWaveLoads / kEntries; j < (e + 1) * kWaveLoads / kEntries; ++j)
+                    from[j] = base + (ok ? g.off[j] : (uint32_t)(lane & 15) * 16);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int pg = page_of(c, first + i * kLoadRows + lane / kRowLanes);
-                e.at[i] = pg < c.table_width ? t.table[pg] : -1;
+            for (int j = 0; j < kWaveLoads; ++j) {
+                const int r = j * kLoadRows + lane / kChunks;
+                const int64_t at = slot_offset(c, g.table, tile * kKeys + g.row0 + r, 0);
+                from[j] = at < 0 ? tp.zeros
+                                 : g.base + at * kItem +
+                                       (((lane % kChunks) ^ swizzle<D, kE4m3>(r)) << 4);
             }
         }
-    }
-    __device__ static __forceinline__ void load(const PagedCache &c, const Task &t, int tile,
-                                                const Entry &e, Regs &g) {
-        const int lane = threadIdx.x & (kWave - 1);
-        const int first = tile * kTileKeys + wave_id() * 16;
-        const bool together = c.page % 16 == 0;
-        const char *kp = static_cast<const char *>(c.k), *vp = static_cast<const char *>(c.v);
-        g.holes = 0;
+        slots.pick(number, [&](char *slot) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = i * kLoadRows + lane / kRowLanes;
-            const int pos = first + r;
-            const int at = together ? e.at[0] : e.at[i];
-            const int pg = together ? page_of(c, first) : page_of(c, pos);
-            const bool named = at >= 0 && at < c.pages;
-            const bool here = named && pos >= t.lo && pos < t.hi;
-            // one bit per row: lanes of the row's first chunk
-            const uint64_t no = __ballot(!named);
-#pragma unroll
-            for (int x = 0; x < kLoadRows; ++x)
-                g.holes |= (int)(no >> (x * kRowLanes) & 1) << (i * kLoadRows + x);
-            g.k[i] = u32x4{0u, 0u, 0u, 0u};
-            g.v[i] = u32x4{0u, 0u, 0u, 0u};
-            if (here) {
-                const int64_t off =
-                    ((int64_t)at * c.page_stride + (int64_t)(pos - pg * c.page) * c.slot_stride +
-                     t.head_off) * kItem + (lane % kRowLanes) * 16;
-                g.k[i] = *reinterpret_cast<const u32x4 *>(kp + off);
-                g.v[i] = *reinterpret_cast<const u32x4 *>(vp + off);
-            }
-        }
+            for (int j = 0; j < kWaveLoads; ++j)
+                dma(from[j], slot + (w * kWaveLoads + j) * 1024);
+        });
     }
-    __device__ static __forceinline__ u32x4 widen(uint32_t a, uint32_t b) {
-        return u32x4{
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false)),
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true)),
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false)),
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true))};
-    }
-    __device__ static __forceinline__ void put(char *buf, int r, int lane, u32x4 x, bool scrub,
-                                               bool &bad) {
-        const int f = swizzle<D>(r), c = lane % kRowLanes;
-        char *row = buf + r * (D * 2);
-        if (kE4m3) {  // 16 values are two chunks of bf16, exactly
-            u32x4 y = widen(x[0], x[1]), z = widen(x[2], x[3]);
-            if (scrub) bad = scrubbed(y) | scrubbed(z);
-            *reinterpret_cast<u32x4 *>(row + (((2 * c) ^ f) << 4)) = y;
-            *reinterpret_cast<u32x4 *>(row + (((2 * c + 1) ^ f) << 4)) = z;
-        } else {
-            if (scrub) bad = scrubbed(x);
-            *reinterpret_cast<u32x4 *>(row + ((c ^ f) << 4)) = x;
-        }
-    }
-    // Sets what is not finite to 0; whether anything was.
-    __device__ static __forceinline__ bool scrubbed(u32x4 &x) {
-        u16x2 top = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[i] & 0x7F807F80u));
-        const bool bad = top[0] == 0x7F80 || top[1] == 0x7F80;
-        if (bad) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if ((x[i] & 0x7F80u) == 0x7F80u) x[i] &= 0xFFFF0000u;
-                if ((x[i] & 0x7F800000u) == 0x7F800000u) x[i] &= 0xFFFFu;
-            }
-        }
-        return bad;
-    }
+
     // Whether some row of the block does not see some key of the tile that another
-    // one sees. There a weight of zero must keep out whatever the value is, which
-    // zero times an infinity or NaN would not: values that are not finite are
-    // staged as 0, and add_bad adds them to the rows that see them.
+    // one sees, or the tile holds rows that none sees. There a weight of zero must
+    // keep out whatever the value is, which zero times an infinity or NaN would
+    // not: values that are not finite are set to 0 in LDS, and add_bad adds them to
+    // the rows that see them.
     __device__ static __forceinline__ bool partial(const AttendParams &p, const Task &t, int tile) {
-        const int k0 = tile * kTileKeys;
-        return k0 + kTileKeys - 1 > t.first || (p.window > 0 && k0 <= t.final - p.window);
+        const int k0 = tile * kKeys;
+        return k0 + kKeys - 1 > t.first || (p.window > 0 && k0 <= t.final - p.window);
     }
-    __device__ static __forceinline__ void store(Lds &s, int buf, const Regs &g, bool scrub) {
-        const int lane = threadIdx.x & (kWave - 1);
-        uint32_t marks = (uint32_t)g.holes;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = wave_id() * 16 + i * kLoadRows + lane / kRowLanes;
-            bool bad = false;
-            put(s.stage[buf][0], r, lane, g.k[i], false, bad);
-            put(s.stage[buf][1], r, lane, g.v[i], scrub, bad);
-            const uint64_t m = __ballot(bad);
-            if (m) {
-#pragma unroll
-                for (int x = 0; x < kLoadRows; ++x)
-                    marks |= (m >> (x * kRowLanes) & ((1ull << kRowLanes) - 1))
-                                 ? 0x10000u << (i * kLoadRows + x) : 0u;
-            }
+    __device__ static __forceinline__ bool bad_word(uint32_t x) {
+        if (kE4m3) {  // a byte of 0x7F without its sign
+            const uint32_t y = (x & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu;
+            return ((y - 0x01010101u) & ~y & 0x80808080u) != 0;
         }
-        if (lane == 0) s.marks[buf][wave_id()] = marks;
+        return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
     }
-
-    // The values that `store` left out, from the cache again: to the rows that
-    // see them. Their weights do not matter: the sum is not finite with any.
-    __device__ static __forceinline__ void add_bad(const uint32_t *marks, int tile, int sub,
-                                                   int keys, const AttendParams &p, const Task &t,
-                                                   State &st) {
-        const int h = (threadIdx.x >> 5) & 1;
+    __device__ static __forceinline__ uint32_t good_part(uint32_t x) {
+        if (kE4m3) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((x >> (8 * i) & 0x7Fu) == 0x7Fu) x &= ~(0xFFu << (8 * i));
+            return x;
+        }
+        if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+        if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
+        return x;
+    }
+    // By each wave that stages values, on its own rows, once they have arrived.
+    __device__ static __forceinline__ void scrub(Lds &s, const Slots &slots, int n, int lane) {
+        const int w = wave_id();
+        if (w < kStagers) return;
+        uint64_t rows = 0;
+        typedef __attribute__((address_space(3))) u32x4 *Words;
+        const uint32_t slot = slots.address(n);
 #pragma unroll 1
-        for (int y = sub * 32; y < sub * 32 + keys; ++y) {
-            if (!(marks[y / 16] >> (16 + y % 16) & 1)) continue;
-            const int key = tile * kTileKeys + y, pg = page_of(p.c, key);
-            const int64_t at = (int64_t)t.table[pg] * p.c.page_stride + t.head_off +
-                               (int64_t)(key - pg * p.c.page) * p.c.slot_stride;
+        for (int j = 0; j < kWaveLoads; ++j) {
+            const Words at = (Words)(uintptr_t)(slot + (w * kWaveLoads + j) * 1024 + lane * 16);
+            u32x4 x = *at;
+            const bool bad = bad_word(x[0]) || bad_word(x[1]) || bad_word(x[2]) || bad_word(x[3]);
+            const uint64_t m = __ballot(bad);
+            if (m == 0) continue;
+            if (bad) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = good_part(x[i]);
+                *at = x;
+            }
+            for (int r = 0; r < kLoadRows; ++r)
+                if (m >> (r * kChunks) & ((1ull << kChunks) - 1))
+                    rows |= 1ull << (j * kLoadRows + r);
+        }
+        if (lane == 0) s.bad[n][w - kStagers] = rows;
+        wait_loads<63>();  // LDS accesses only
+    }
+    // The values that scrub left out of 32 keys, from the cache again: to the
+    // rows that see them. Their weights do not matter: the sum is not finite with
+    // any.
+    __device__ static __forceinline__ void add_bad(const uint64_t *bad, int tile, int sub,
+                                                   const AttendParams &p, const Task &t,
+                                                   State &st, int lane) {
+        const int h = lane >> 5;
+#pragma unroll 1
+        for (int y = sub * 32; y < sub * 32 + 32; ++y) {
+            if (!(bad[y / kWaveRows] >> (y % kWaveRows) & 1)) continue;
+            const int key = tile * kKeys + y;
+            const int64_t at = slot_offset(p.c, t.table, key, 0);
+            if (at < 0) continue;
             const bool see = visible(p, t, key);
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const float v = load1<kE4m3>(p.c.v, at + d * 32 + 8 * (r / 4) + 4 * h + (r & 3));
+                    const float v = load1<kE4m3>(
+                        p.c.v, at + t.head_off + d * 32 + 8 * (r / 4) + 4 * h + (r & 3));
                     st.o[d][r] += see && !(fabsf(v) < INFINITY) ? v : 0.f;
                     __builtin_amdgcn_sched_barrier(0);  // one at a time: registers, not speed
                 }
         }
     }
+
+    // ------------------------------------------------------------- compute
     // Whether this lane's query row sees a position that has a page.
     __device__ static __forceinline__ bool visible(const AttendParams &p, const Task &t, int key) {
         return key <= t.pos && key >= t.lo && key < t.hi &&
                (p.window == 0 || key > t.pos - p.window);
     }
-
-    // One staged tile against the wave's 32 query rows: kSub subtiles of 32
-    // keys from subtile `sub` on.
-    template <int kSub>
-    __device__ static __forceinline__ void compute(Lds &s, int buf, int tile, int sub,
-                                                   const AttendParams &p, const Task &t,
-                                                   State &st) {
+    __device__ static __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
+        const u32x4 x = {
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true))};
+        return __builtin_bit_cast(bf16x8, x);
+    }
+    // Elements 16 ks .. 16 ks + 15 of 32 keys (rows), 8 of them for either half of
+    // the wave.
+    __device__ static __forceinline__ bf16x8 keys_of(const char *rows, int ks, int lane) {
+        const int r = lane & 31, h = lane >> 5;
+        const int f = swizzle<D, kE4m3>(r);
+        if (kE4m3) {
+            const i32x2 x =
+                *reinterpret_cast<const i32x2 *>(rows + r * kRow + ((ks ^ f) << 4) + h * 8);
+            return widen((uint32_t)x[0], (uint32_t)x[1]);
+        }
+        return *reinterpret_cast<const bf16x8 *>(rows + r * kRow + (((2 * ks + h) ^ f) << 4));
+    }
+    // V^T of 16 keys (rows from 16 kk on): elements 32 d .. 32 d + 31, and of the keys
+    // 4h .. 4h + 3 and 8 + 4h .. 8 + 4h + 3 for half h, the places of their weights.
+    // A row of 8 bits takes one transposing read, one of 16 two.
+    static constexpr int kReads = kE4m3 ? 1 : 2;
+    static constexpr int kValueReads = kReads * (D / 32);  // of 16 keys
+    struct ValueAddresses {
+        uint32_t at[kValueReads];
+    };
+    __device__ static __forceinline__ ValueAddresses value_addresses(uint32_t base, int lane) {
+        const int i16 = lane & 15, grp = (lane >> 4) & 1, h = lane >> 5;
+        ValueAddresses v;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int e = 0; e < kReads; ++e) {
+                const int r = kE4m3 ? 8 * (i16 >> 3) + 4 * h + ((i16 >> 1) & 3)
+                                    : 8 * e + 4 * h + (i16 >> 2);
+                const int c = kE4m3 ? 2 * d + grp : 4 * d + 2 * grp + ((i16 & 3) >> 1);
+                v.at[d * kReads + e] = base + (uint32_t)(r * kRow + ((c ^ swizzle<D, kE4m3>(r)) << 4) +
+                                                         (i16 & 1) * 8);
+            }
+        return v;
+    }
+    // The reads are issued and waited for in one piece: as builtins they would wait
+    // for every load into LDS under way (the compiler does not know which slot they
+    // read), and the tiles ahead with them.
+    template <int kOffset>
+    __device__ static __forceinline__ void read_values(const ValueAddresses &v,
+                                                       i32x2 (&x)[kValueReads]) {
+        if constexpr (kE4m3 && D == 64) {
+            asm volatile("ds_read_b64_tr_b8 %0, %2 offset:%c4\n\t"
+                         "ds_read_b64_tr_b8 %1, %3 offset:%c4\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(x[0]), "=&v"(x[1])
+                         : "v"(v.at[0]), "v"(v.at[1]), "i"(kOffset));
+        } else if constexpr (kE4m3) {
+            asm volatile("ds_read_b64_tr_b8 %0, %4 offset:%c8\n\t"
+                         "ds_read_b64_tr_b8 %1, %5 offset:%c8\n\t"
+                         "ds_read_b64_tr_b8 %2, %6 offset:%c8\n\t"
+                         "ds_read_b64_tr_b8 %3, %7 offset:%c8\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+                         : "v"(v.at[0]), "v"(v.at[1]), "v"(v.at[2]), "v"(v.at[3]), "i"(kOffset));
+        } else if constexpr (D == 64) {
+            asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%c8\n\t"
+                         "ds_read_b64_tr_b16 %1, %5 offset:%c8\n\t"
+                         "ds_read_b64_tr_b16 %2, %6 offset:%c8\n\t"
+                         "ds_read_b64_tr_b16 %3, %7 offset:%c8\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+                         : "v"(v.at[0]), "v"(v.at[1]), "v"(v.at[2]), "v"(v.at[3]), "i"(kOffset));
+        } else {
+            asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %1, %9 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %2, %10 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %3, %11 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %4, %12 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %5, %13 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %6, %14 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %7, %15 offset:%c16\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]),
+                           "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+                         : "v"(v.at[0]), "v"(v.at[1]), "v"(v.at[2]), "v"(v.at[3]), "v"(v.at[4]),
+                           "v"(v.at[5]), "v"(v.at[6]), "v"(v.at[7]), "i"(kOffset));
+        }
+    }
+    __device__ static __forceinline__ bf16x8 value_of(const i32x2 (&x)[kValueReads], int d) {
+        if constexpr (kE4m3) return widen((uint32_t)x[d][0], (uint32_t)x[d][1]);
+        const u32x4 y = {(uint32_t)x[2 * d][0], (uint32_t)x[2 * d][1], (uint32_t)x[2 * d + 1][0],
+                         (uint32_t)x[2 * d + 1][1]};
+        return __builtin_bit_cast(bf16x8, y);
+    }
+    template <int kSub, int kk>
+    __device__ static __forceinline__ void add_values(const ValueAddresses &v, const bf16x8 *w,
+                                                      State &st) {
+        i32x2 x[kValueReads];
+        read_values<16 * kk * kRow>(v, x);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+            st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value_of(x, d), w[kk], st.o[d], 0, 0,
+                                                              0);
+        if constexpr (kk + 1 < 2 * kSub) add_values<kSub, kk + 1>(v, w, st);
+    }
+    // Whether a page of positions [k0, k1) is missing from the table.
+    __device__ static __forceinline__ bool holes(const PagedCache &c, const int32_t *table, int k0,
+                                                 int k1, bool together) {
+        if (!together) return true;  // looked up key by key
         const int lane = threadIdx.x & (kWave - 1);
+        const int last = page_of(c, k1 - 1);
+        bool any = last >= c.table_width;
+#pragma unroll 4
+        for (int i = page_of(c, k0) + lane; i <= last; i += kWave)
+            any |= i < c.table_width && !named(c, table[i]);
+        return __any(any);
+    }
+
+    // kSub times 32 keys, from key 32 * sub of a staged tile on, against the wave's
+    // 32 query rows.
+    template <int kSub>
+    __device__ static __forceinline__ void compute(const Slots &slots, int number, int tile, int sub,
+                                                   const AttendParams &p, const Task &t,
+                                                   State &st, int lane) {
         const int h = lane >> 5;
-        const int k0 = tile * kTileKeys + sub * 32, k1 = k0 + kSub * 32 - 1;
-        const uint32_t *ho = s.marks[buf];
-        const uint32_t marks = __builtin_amdgcn_readfirstlane(ho[0] | ho[1] | ho[2] | ho[3]);
+        const int k0 = tile * kKeys + sub * 32, k1 = k0 + kSub * 32 - 1;
         if (k0 > t.pos_max || k0 >= t.hi || k1 < t.lo ||
             (p.window > 0 && k1 <= t.pos_min - p.window))
             return;
-        const bool whole = k1 <= t.pos_min && k1 < t.hi && k0 >= t.lo && marks == 0 &&
+        const bool whole = k1 <= t.pos_min && k1 < t.hi && k0 >= t.lo && !t.hole &&
                            (p.window == 0 || k0 > t.pos_max - p.window);
-        const char *kb = s.stage[buf][0] + sub * 32 * D * 2;
-        const char *vb = s.stage[buf][1] + sub * 32 * D * 2;
         // scores, transposed: keys down the registers, queries across the lanes
         f32x16 x[kSub];
 #pragma unroll
         for (int i = 0; i < kSub; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[i][r] = 0.f;
-        {
-            const int row = lane & 31;
-            const char *base = kb + row * (D * 2);
-            const int f = swizzle<D>(row) ^ h;
+        slots.pick(number, [&](const char *slot) {
+            const char *kb = slot + sub * 32 * kRow;
+            // four operands are on their way from LDS behind the product at work
+            constexpr int kAhead = 4, kProducts = D / 16 * kSub;
+            bf16x8 a[kAhead];
+            auto read = [&](int u) {
+                a[u % kAhead] = keys_of(kb + u % kSub * 32 * kRow, u / kSub, lane);
+            };
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
+            for (int u = 0; u < kAhead; ++u) read(u);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < kSub; ++i) {
-                    const bf16x8 a = *reinterpret_cast<const bf16x8 *>(
-                        base + i * 32 * D * 2 + ((f ^ (2 * ks)) << 4));
-                    x[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, st.q[ks], x[i], 0, 0, 0);
-                }
+            for (int u = 0; u < kProducts; ++u) {
+                x[u % kSub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[u % kAhead], st.q[u / kSub],
+                                                                      x[u % kSub], 0, 0, 0);
+                if (u + kAhead < kProducts) read(u + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
+        });
         if (!whole) {
+            asm volatile("");  // a branch: few tiles are masked, selects would cost all of them
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
-                const int w = (sub + i) * 2;
-                const uint32_t no = (ho[w] & 0xFFFFu) | (ho[w + 1] << 16);
+                uint32_t no = 0;
+                if (t.hole)
+                    no = (uint32_t)__ballot(
+                        slot_offset(p.c, t.table, k0 + i * 32 + (lane & 31), 0) < 0);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int y = 8 * (r / 4) + 4 * h + (r & 3);
-                    const int key = k0 + i * 32 + y;
-                    x[i][r] = visible(p, t, key) && !(no >> y & 1) ? x[i][r] : -INFINITY;
+                    x[i][r] = visible(p, t, k0 + i * 32 + y) && !(no >> y & 1) ? x[i][r]
+                                                                               : -INFINITY;
                 }
             }
         }
@@ -514,58 +734,23 @@ struct Tiles {
             }
         }
         st.l += sum;
-        {
-            const int i16 = lane & 15, grp = (lane >> 4) & 1;
-            const int f = (2 * grp + ((i16 & 3) >> 1)) ^ (swizzle<D>(i16 >> 2) | h);
-            const char *base = vb + (4 * h + (i16 >> 2)) * (D * 2) + (i16 & 1) * 8;
-#pragma unroll
-            for (int kk = 0; kk < kSub * 2; ++kk) {
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d) {
-                    s16x4 half[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const char *at =
-                            base + (16 * kk + 8 * e) * (D * 2) + ((f ^ (4 * d) ^ (2 * e)) << 4);
-                        half[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4 *)at);
-                    }
-                    const s16x8 a = __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, a), w[kk], st.o[d], 0, 0, 0);
-                }
-            }
-        }
-        if (marks >> 16) add_bad(ho, tile, sub, kSub * 32, p, t, st);
-    }
-
-    template <int kSub>
-    __device__ static __forceinline__ void run(Lds &s, const AttendParams &p, const Task &t,
-                                               int tile, int n, int sub, State &st) {
-        Entry e;
-        Regs g;
-        lookup(p.c, t, tile, e);
-        load(p.c, t, tile, e, g);
-        if (n > 1) lookup(p.c, t, tile + 1, e);
-        store(s, 0, g, partial(p, t, tile));
-        for (int i = 0; i < n; ++i) {
-            if (i + 1 < n) {
-                load(p.c, t, tile + i + 1, e, g);
-                if (i + 2 < n) lookup(p.c, t, tile + i + 2, e);
-            }
-            __syncthreads();
-            if (t.active) compute<kSub>(s, i & 1, tile + i, sub, p, t, st);
-            // the other buffer's readers passed the barrier above
-            if (i + 1 < n) store(s, (i + 1) & 1, g, partial(p, t, tile + i + 1));
-        }
-        __syncthreads();
+        add_values<kSub, 0>(
+            value_addresses(slots.address(number) + kHalfSlot + sub * 32 * kRow, lane), w, st);
     }
 };
 
-template <int D, bool kE4m3>
-__global__ __launch_bounds__(kTileThreads, kTileWgsPerCu) void attend_tile_kernel(TileParams tp) {
-    using T = Tiles<D, kE4m3>;
+template <int D, bool kE4m3, bool kWide>
+__global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileParams tp) {
+    using T = Tiles<D, kE4m3, kWide>;
+    using Unit = typename T::Unit;
+    constexpr int kBlockRows = T::kBlockRows, kSlots = T::kSlots, kWaveLoads = T::kWaveLoads;
+    constexpr int kTileThreads = T::kThreads, kTileWaves = T::kWaves;
     __shared__ typename T::Lds s;
+    __shared__ __attribute__((aligned(1024))) char slot0[kSlotBytes];
+    __shared__ __attribute__((aligned(1024))) char slot1[kSlotBytes];
+    __shared__ __attribute__((aligned(1024))) char slot2[kWide ? kSlotBytes : 16];
+    __shared__ __attribute__((aligned(1024))) char slot3[kWide ? kSlotBytes : 16];
+    const typename T::Slots slots = {slot0, slot1, slot2, slot3};
     const AttendParams &p = tp.a;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = T::wave_id();
     const int G = p.Hq / p.Hkv, wgs = gridDim.x;
@@ -574,14 +759,14 @@ __global__ __launch_bounds__(kTileThreads, kTileWgsPerCu) void attend_tile_kerne
     if (tid == 0) s.before[0] = 0;
     if ((int64_t)p.max_rows * G <= kBlockRows) {
         for (int b = tid; b < p.B; b += kTileThreads) {
-            const Request q = load_request(p, b);
-            s.before[b + 1] = q.M > 0 ? (uint64_t)block_of(p, q, 0).tiles * p.Hkv : 0;
+            const Request q = load_request<kBlockRows>(p, b);
+            s.before[b + 1] = q.M > 0 ? (uint64_t)block_of<kBlockRows, T::kKeys>(p, q, 0).tiles * p.Hkv : 0;
         }
     } else {
         for (int b = wave; b < p.B; b += kTileWaves) {
-            const Request q = load_request(p, b);
+            const Request q = load_request<kBlockRows>(p, b);
             uint64_t n = 0;
-            for (int i = lane; i < q.blocks; i += kWave) n += block_of(p, q, i).tiles;
+            for (int i = lane; i < q.blocks; i += kWave) n += block_of<kBlockRows, T::kKeys>(p, q, i).tiles;
             n = wave_incl_sum_u64(n);
             if (lane == kWave - 1) s.before[b + 1] = n * p.Hkv;
         }
@@ -619,29 +804,27 @@ __global__ __launch_bounds__(kTileThreads, kTileWgsPerCu) void attend_tile_kerne
     const int share = used / 8 + (xcd < used % 8);
     if (nth >= share) return;
     const int g = xcd * (used / 8) + (xcd < used % 8 ? xcd : used % 8) + nth;
-    uint64_t cur = (uint64_t)g * per;
-    const uint64_t end = cur + per < total ? cur + per : total;
+    const uint64_t start = (uint64_t)g * per;
+    const uint64_t end = start + per < total ? start + per : total;
 
     // the unit of the first tile
-    int b = 0;
+    Unit next;
     {
-        int hi = p.B - 1;
+        int b = 0, hi = p.B - 1;
         while (b < hi) {
             const int mid = (b + hi) >> 1;
-            if (s.before[mid + 1] <= cur) b = mid + 1;
+            if (s.before[mid + 1] <= start) b = mid + 1;
             else hi = mid;
         }
-    }
-    Request q = load_request(p, b);
-    int head, blk = 0, t0;
-    {
-        const uint64_t in = cur - s.before[b];
+        const Request q = load_request<kBlockRows>(p, b);
+        const uint64_t in = start - s.before[b];
         const uint64_t each = (uint64_t)udiv64((int64_t)(s.before[b + 1] - s.before[b]), p.Hkv);
-        head = (int)udiv64((int64_t)in, (int64_t)each);
+        const int head = (int)udiv64((int64_t)in, (int64_t)each);
         uint64_t rest = in - (uint64_t)head * each;
+        int blk = 0;
         for (int i0 = 0; q.blocks > 1; i0 += kWave) {
             const int i = i0 + lane;
-            const uint64_t n = i < q.blocks ? (uint64_t)block_of(p, q, i).tiles : 0;
+            const uint64_t n = i < q.blocks ? (uint64_t)block_of<kBlockRows, T::kKeys>(p, q, i).tiles : 0;
             const uint64_t in64 = wave_incl_sum_u64(n);
             const uint64_t all = __shfl(in64, kWave - 1, kWave);
             if (rest < all || i0 + kWave >= q.blocks) {
@@ -653,100 +836,197 @@ __global__ __launch_bounds__(kTileThreads, kTileWgsPerCu) void attend_tile_kerne
             }
             rest -= all;
         }
-        t0 = (int)rest;
+        next.b = __builtin_amdgcn_readfirstlane(b);
+        next.head = __builtin_amdgcn_readfirstlane(head);
+        next.blk = __builtin_amdgcn_readfirstlane(blk);
+        next.q = scalar_request<kBlockRows>(p, next.b);
+        next.k = block_of<kBlockRows, T::kKeys>(p, next.q, next.blk);
+        next.tile = next.k.tile + __builtin_amdgcn_readfirstlane((int)rest);
+        next.left = next.k.tiles - (next.tile - next.k.tile);
     }
-    while (cur < end) {
-        b = __builtin_amdgcn_readfirstlane(b);
-        head = __builtin_amdgcn_readfirstlane(head);
-        blk = __builtin_amdgcn_readfirstlane(blk);
-        t0 = __builtin_amdgcn_readfirstlane(t0);
-        const Block k = block_of(p, q, blk);
-        const int left = k.tiles - t0;
-        const int n = __builtin_amdgcn_readfirstlane(
-            (uint64_t)left < end - cur ? left : (int)(end - cur));
-        const int m0 = blk * kBlockRows;
-        const int rows = q.M - m0 < kBlockRows ? q.M - m0 : kBlockRows;
-        // over 64 rows: a wave per 32 rows, every key; up to 64: two waves per 32
-        // rows, each with half of a tile's keys
-        const bool wide = rows > 64;
-        const int qt = wide ? wave : wave & 1, kg = wide ? 0 : wave >> 1;
-        const int mine = qt * 32 + (lane & 31);
-        const int m = m0 + mine;
-        const bool valid = mine < rows;
-        const int j = m / G;
-        const int64_t row = q.start + j;
-        const int hq = head * G + (m - j * G);
+    auto begin_next = [&](Unit &u) {
+        if (++u.blk == u.q.blocks) {
+            u.blk = 0;
+            if (++u.head == p.Hkv) {
+                u.head = 0;
+                do u.q = scalar_request<kBlockRows>(p, ++u.b);
+                while (u.q.blocks == 0);
+            }
+        }
+        u.k = block_of<kBlockRows, T::kKeys>(p, u.q, u.blk);
+        u.tile = u.k.tile;
+        u.left = u.k.tiles;
+    };
 
-        typename T::Task t;
-        t.table = p.c.table + (int64_t)b * p.c.table_width;
-        t.head_off = (int64_t)head * p.c.head_stride;
-        t.lo = k.lo;
-        t.hi = k.hi;
-        t.ctx = q.ctx;
-        t.pos = q.ctx + j;
-        t.first = q.ctx + m0 / G;
-        t.final = q.ctx + (m0 + rows - 1) / G;
-        t.pos_min = q.ctx + (m0 + qt * 32) / G;
+    // The stager runs three tiles ahead; past the last one it repeats it, so that
+    // a fixed number of loads is always on its way.
+    const int count = (int)(end - start);
+    int staged = 0;
+    typename T::Stager sg;
+    T::stager(tp, sg);
+    Unit ahead = next;
+    T::enter(tp, sg, ahead);
+    T::look_up(tp, sg, ahead.tile);
+    auto stage = [&](int number, int lane) {
+        T::issue(tp, sg, ahead.tile, slots, number, lane);
+        if (++staged < count) {
+            if (--ahead.left == 0) {
+                begin_next(ahead);
+                T::enter(tp, sg, ahead);
+                T::look_up(tp, sg, ahead.tile);
+            } else if (++ahead.tile - sg.batch0 == kWave) {
+                T::look_up(tp, sg, ahead.tile);
+            }
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < kSlots - 1; ++i) stage(i, lane);
+
+    typename T::Task t;
+    typename T::State st;
+    uint64_t cur = start;  // the unit's first tile here
+    int n = 0, rows = 0, qts = 1, kgs = 1, qt = 0, kg = 0, m = 0, hq = 0;
+    int each = 1;  // times 32 keys of a tile for every group of waves
+    int64_t row = 0;
+    bool valid = false;
+
+    // one tile: its arrival, the loads of the third after it, its products
+    auto step = [&](int number) {
+        // addresses are made anew for every tile: kept for all slots they would not
+        // fit the registers
+        int lane = threadIdx.x & (kWave - 1);
+        asm volatile("" : "+v"(lane));
+        const int tile = next.tile;
+        const bool part = T::partial(p, t, tile);
+        wait_loads<(kSlots - 2) * kWaveLoads>();
+        if (part) T::scrub(s, slots, number, lane);
+        asm volatile("" ::: "memory");  // no access to LDS is moved across the barrier
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        stage((number + kSlots - 1) & (kSlots - 1), lane);
+        if (t.active) {
+            if constexpr (kWide) {
+#pragma unroll 1
+                for (int sub = 0; sub < T::kKeys / 32; sub += 2)
+                    T::template compute<2>(slots, number, tile, sub, p, t, st, lane);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < each; ++i)
+                    T::template compute<1>(slots, number, tile, kg * each + i, p, t, st, lane);
+            }
+            if (part) {
+                const uint64_t *bad = s.bad[number];
+                uint64_t any = 0;
+#pragma unroll
+                for (int i = 0; i < T::kStagers; ++i) any |= bad[i];
+                if (any) {
+#pragma unroll 1
+                    for (int i = 0; i < each; ++i)
+                        T::add_bad(bad, tile, kg * each + i, p, t, st, lane);
+                }
+            }
+        }
+        ++next.tile;
+    };
+
+    auto begin = [&]() {
+        const int m0 = next.blk * kBlockRows;
+        rows = next.q.M - m0 < kBlockRows ? next.q.M - m0 : kBlockRows;
+        const uint64_t rest = end - cur;
+        n = (uint64_t)next.left < rest ? next.left : (int)rest;
+        // 32 query rows a wave; where fewer than eight waves hold them all, the
+        // others take their share of a tile's keys
+        constexpr int kLogWaves = kWide ? 3 : 2;
+        const int lq = kWide ? 3 : rows > 64 ? 2 : rows > 32 ? 1 : 0;
+        constexpr int kLogKeys = T::kKeys == 64 ? 1 : T::kKeys == 128 ? 2 : 3;  // of 32 keys
+        const int lk = kLogWaves - lq < kLogKeys ? kLogWaves - lq : kLogKeys;
+        qts = 1 << lq;
+        kgs = 1 << lk;
+        each = 1 << (kLogKeys - lk);
+        qt = wave & (qts - 1);
+        kg = wave >> lq;
+        const int mine = qt * 32 + (lane & 31);
+        m = m0 + mine;
+        valid = mine < rows;
+        const int j = m / G;
+        row = next.q.start + j;
+        hq = next.head * G + (m - j * G);
+
+        t.table = p.c.table + (int64_t)next.b * p.c.table_width;
+        t.head_off = (int64_t)next.head * p.c.head_stride;
+        t.lo = next.k.lo;
+        t.hi = next.k.hi;
+        t.first = next.k.first;
+        t.final = next.k.final;
+        t.pos = next.q.ctx + j;
+        t.pos_min = next.q.ctx + (m0 + qt * 32) / G;
         const int m_last = (qt * 32 + 31 < rows - 1 ? qt * 32 + 31 : rows - 1) + m0;
-        t.pos_max = q.ctx + m_last / G;
-        t.active = qt * 32 < rows;
+        t.pos_max = next.q.ctx + m_last / G;
+        t.active = kg < kgs && qt * 32 < rows;
         // a negative scale turns the queries' signs, none at all their values to 0
         const float scale = p.scale * p.c.k_scale;
         t.c = (scale == 0.f ? 1.f : fabsf(scale)) * kLog2e;
         const uint32_t keep = scale == 0.f ? 0u : 0xFFFFFFFFu;
         const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
-
-        typename T::State st;
         st.m = -INFINITY;
         st.l = 0.f;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) st.o[d][r] = 0.f;
-        {
-            const uint16_t *src = p.q + row * p.q_row + hq * p.q_head + (lane >> 5) * 8;
+        const uint16_t *src = p.q + row * p.q_row + hq * p.q_head + (lane >> 5) * 8;
+        u32x4 x[D / 16];
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                u32x4 x = {0u, 0u, 0u, 0u};
-                if (valid) x = *reinterpret_cast<const u32x4 *>(src + ks * 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = (x[i] & keep) ^ flip;
-                st.q[ks] = __builtin_bit_cast(bf16x8, x);
-            }
+        for (int ks = 0; ks < D / 16; ++ks) {
+            x[ks] = u32x4{0u, 0u, 0u, 0u};
+            if (valid && t.active) x[ks] = *reinterpret_cast<const u32x4 *>(src + ks * 16);
         }
-        if (wide) T::template run<2>(s, p, t, k.tile + t0, n, 0, st);
-        else T::template run<1>(s, p, t, k.tile + t0, n, kg, st);
-        st.l = half_sum(st.l);
+        const int k0 = next.tile * T::kKeys, k1 = (next.tile + n) * T::kKeys;
+        t.hole = T::holes(p.c, t.table, k0 > t.lo ? k0 : t.lo, k1 < t.hi ? k1 : t.hi, tp.together);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[ks][i] = (x[ks][i] & keep) ^ flip;
+            st.q[ks] = __builtin_bit_cast(bf16x8, x[ks]);
+        }
+    };
 
-        if (!wide) {  // the two halves of the keys meet
-            float *mem = s.join[qt];
-            if (kg == 1 && t.active) {
+    // the unit's tiles here are done: joins the waves, stores the rows or leaves
+    // them for the last workgroup
+    auto finish = [&]() {
+        st.l = half_sum(st.l);
+        // the groups of keys meet, 32 elements of all rows at a time
+        for (int half = kWide ? 0 : kgs / 2; half >= 1; half /= 2) {
+            const bool from = t.active && kg >= half && kg < 2 * half;
+            const bool to = t.active && kg < half;
+            const int at = (qt + qts * (from ? kg - half : kg)) * kWave + lane;  // below kTileThreads / 2
+            float a = 0.f, c = 0.f;
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d)
+            for (int d = 0; d < D / 32; ++d) {
+                __syncthreads();
+                if (from) {
+                    if (d == 0) s.ml[at] = f32x2{st.m, st.l};
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) mem[(d * 16 + r) * kWave + lane] = st.o[d][r];
-                mem[(D / 2) * kWave + lane] = st.m;
-                mem[(D / 2 + 1) * kWave + lane] = st.l;
-            }
-            __syncthreads();
-            if (kg == 0 && t.active) {
-                const float om = mem[(D / 2) * kWave + lane], ol = mem[(D / 2 + 1) * kWave + lane];
-                const float top = fmaxf(st.m, om);
-                const float a = st.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.m - top);
-                const float c = om == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(om - top);
-                st.m = top;
-                st.l = st.l * a + ol * c;
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d)
+                    for (int r = 0; r < 16; ++r) s.join[r * (kTileThreads / 2) + at] = st.o[d][r];
+                }
+                __syncthreads();
+                if (to) {
+                    if (d == 0) {
+                        const f32x2 o = s.ml[at];
+                        const float top = fmaxf(st.m, o[0]);
+                        a = st.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.m - top);
+                        c = o[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(o[0] - top);
+                        st.m = top;
+                        st.l = st.l * a + o[1] * c;
+                    }
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        st.o[d][r] = st.o[d][r] * a + mem[(d * 16 + r) * kWave + lane] * c;
+                        st.o[d][r] = st.o[d][r] * a + s.join[r * (kTileThreads / 2) + at] * c;
+                }
             }
-            __syncthreads();
         }
-        const bool owner = kg == 0 && t.active && valid;
-        if (n == k.tiles) {
-            if (owner) {
+        if (n == next.k.tiles) {
+            if (kg == 0 && t.active && valid) {
                 const float norm = st.l > 0.f ? p.c.v_scale / st.l : 0.f;
                 uint16_t *o = p.out + (row * p.Hq + hq) * D + (lane >> 5) * 4;
 #pragma unroll
@@ -760,90 +1040,178 @@ __global__ __launch_bounds__(kTileThreads, kTileWgsPerCu) void attend_tile_kerne
                         *reinterpret_cast<uint64_t *>(o + d * 32 + 2 * r) = y;
                     }
             }
-        } else {
-            const uint64_t unit = cur - t0;
-            const int g0 = (int)udiv64((int64_t)unit, (int64_t)per);
-            const int g1 = (int)udiv64((int64_t)(unit + k.tiles - 1), (int64_t)per);
-            const int64_t slot = slot_floats(tp.slot_rows, D);
-            auto slot_of = [&](int w) { return tp.slots + slot * (2 * (int64_t)w + (w == g0)); };
-            if (owner) {
-                float *to = slot_of(g);
-                if (lane < 32) store_coherent(to + 2 * mine, st.m, st.l);
-                to += 2 * tp.slot_rows + (int64_t)mine * D + (lane >> 5) * 4;
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        store_coherent(to + d * 32 + 2 * r, st.o[d][r], st.o[d][r + 1]);
-                        store_coherent(to + d * 32 + 2 * r + 2, st.o[d][r + 2], st.o[d][r + 3]);
-                    }
-            }
-            __builtin_amdgcn_s_waitcnt(0);  // the partial results are at the coherence point
-            __syncthreads();
-            if (tid == 0) {
-                const unsigned old = __hip_atomic_fetch_add(tp.arrivals + g0, (unsigned)n,
-                                                            __ATOMIC_RELAXED,
-                                                            __HIP_MEMORY_SCOPE_AGENT);
-                s.last = old + (unsigned)n == (unsigned)k.tiles;
-                if (s.last)  // zero again for the next call
-                    __hip_atomic_store(tp.arrivals + g0, 0u, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-            }
-            __syncthreads();
-            if (s.last) {
-                for (int i = tid; i < rows * (D / 2); i += kTileThreads) {
-                    const int x = i / (D / 2), d = 2 * (i - x * (D / 2));
-                    float top = -INFINITY;
-                    for (int w = g0; w <= g1; ++w)
-                        top = fmaxf(top, load_coherent(slot_of(w) + 2 * x)[0]);
-                    float l = 0.f, a = 0.f, c = 0.f;
-                    for (int w = g0; w <= g1; ++w) {
-                        const float *from = slot_of(w);
-                        const f32x2 ml = load_coherent(from + 2 * x);
-                        const f32x2 v =
-                            load_coherent(from + 2 * tp.slot_rows + (int64_t)x * D + d);
-                        const float f =
-                            ml[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[0] - top);
-                        l += f * ml[1];
-                        a += f * v[0];
-                        c += f * v[1];
-                    }
-                    const float norm = l > 0.f ? p.c.v_scale / l : 0.f;
-                    const int jj = (m0 + x) / G, hh = head * G + (m0 + x - jj * G);
-                    *reinterpret_cast<uint32_t *>(
-                        p.out + ((int64_t)(q.start + jj) * p.Hq + hh) * D + d) =
-                        pack_bf16(a * norm, c * norm);
-                }
-            }
+            return;
         }
-        // the next unit
-        cur += n;
-        t0 = 0;
-        if (cur < end) {
-            if (++blk == q.blocks) {
-                blk = 0;
-                if (++head == p.Hkv) {
-                    head = 0;
-                    do q = load_request(p, ++b);
-                    while (q.blocks == 0);
-                }
-            }
+        const uint64_t unit = cur - (uint64_t)(next.k.tiles - next.left);
+        const int g0 = (int)udiv64((int64_t)unit, (int64_t)per);
+        const int g1 = (int)udiv64((int64_t)(unit + next.k.tiles - 1), (int64_t)per);
+        const int64_t size = slot_floats(tp.slot_rows, D);
+        auto slot_of = [&](int w) { return tp.slots + size * (2 * (int64_t)w + (w == g0)); };
+        const int m0 = next.blk * kBlockRows;
+        // pairs of elements in the order of the registers, a wave's 64 pairs together
+        constexpr int kPairs = D / 4;  // of a lane
+        if (kg == 0 && t.active) {
+            float *to = slot_of(g);
+            if (lane < 32) store_coherent(to + 2 * (qt * 32 + lane), st.m, st.l);
+            to += 2 * tp.slot_rows + (int64_t)qt * (32 * D) + 2 * lane;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; r += 2)
+                    store_coherent(to + (d * 8 + r / 2) * (2 * kWave), st.o[d][r], st.o[d][r + 1]);
         }
+        __builtin_amdgcn_s_waitcnt(0);  // the partial results are at the coherence point
+        __syncthreads();
+        if (tid == 0) {
+            const unsigned old = __hip_atomic_fetch_add(tp.arrivals + g0, (unsigned)n,
+                                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s.last = old + (unsigned)n == (unsigned)next.k.tiles;
+            if (s.last)  // zero again for the next call
+                __hip_atomic_store(tp.arrivals + g0, 0u, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (!s.last) return;
+        // First the factor of every part and row, as many rows at a time as s.join
+        // holds, then the pairs of elements: 16 loads are on their way a thread,
+        // two parts of eight pairs or, where there are few pairs, 16 parts of one.
+        const int parts = g1 - g0 + 1;
+        constexpr int kTable = 16 * (T::kWaves / 2) * kWave / 2;
+        const int most = kTable / parts;  // 512 parts at most: two rows or more
+        float *factor = s.join, *share = s.join + kTable;
+        for (int r0 = 0; r0 < rows; r0 += most) {
+            const int nr = rows - r0 < most ? rows - r0 : most;
+            f32x2 ml[kTable / T::kThreads];
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kTable / T::kThreads; ++u) {
+                const int i = u * T::kThreads + tid;
+                ml[u] = f32x2{-INFINITY, 0.f};
+                if (i < nr * parts) ml[u] = load_coherent(slot_of(g0 + i / nr) + 2 * (r0 + i % nr));
+            }
+#pragma unroll
+            for (int u = 0; u < kTable / T::kThreads; ++u) {
+                const int i = u * T::kThreads + tid;
+                if (i < nr * parts) share[i] = ml[u][0];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kTable / T::kThreads; ++u) {
+                const int i = u * T::kThreads + tid;
+                if (i >= nr * parts) break;
+                float top = -INFINITY;
+                for (int w = i % nr; w < nr * parts; w += nr) top = fmaxf(top, share[w]);
+                factor[i] = ml[u][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[u][0] - top);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kTable / T::kThreads; ++u) {
+                const int i = u * T::kThreads + tid;
+                if (i < nr * parts) share[i] = factor[i] != 0.f ? factor[i] * ml[u][1] : 0.f;
+            }
+            __syncthreads();
+            const int items = nr * (D / 2);
+            auto place = [&](int i, int &x, int64_t &at) {  // k: half, pair
+                x = i % nr;
+                const int k = i / nr, r = r0 + x;
+                at = 2 * tp.slot_rows + (int64_t)(r >> 5) * (32 * D) + (k >> 1) * (2 * kWave) +
+                     2 * ((r & 31) + 32 * (k & 1));
+            };
+            auto finish_pair = [&](int i, float l, f32x2 v) {
+                const int x = i % nr, k = i / nr, pair = k >> 1;
+                const float norm = l > 0.f ? p.c.v_scale / l : 0.f;
+                const int d = pair / 8 * 32 + pair % 8 / 2 * 8 + (k & 1) * 4 + pair % 2 * 2;
+                const int mm = m0 + r0 + x, jj = mm / G, hh = next.head * G + (mm - jj * G);
+                *reinterpret_cast<uint32_t *>(
+                    p.out + ((int64_t)(next.q.start + jj) * p.Hq + hh) * D + d) =
+                    pack_bf16(v[0] * norm, v[1] * norm);
+            };
+            auto sums = [&](auto pairs_at_once, auto parts_at_once) {
+                constexpr int kPairs = decltype(pairs_at_once)::value;
+                constexpr int kParts = decltype(parts_at_once)::value;
+                for (int i0 = tid; i0 < items; i0 += T::kThreads * kPairs) {
+                    int x[kPairs];
+                    int64_t at[kPairs];
+                    float l[kPairs];
+                    f32x2 v[kPairs];
+#pragma unroll
+                    for (int u = 0; u < kPairs; ++u) {
+                        const int i = i0 + u * T::kThreads;
+                        place(i < items ? i : i0, x[u], at[u]);
+                        l[u] = 0.f;
+                        v[u] = f32x2{0.f, 0.f};
+                    }
+#pragma unroll 1
+                    for (int w0 = 0; w0 < parts; w0 += kParts) {
+                        f32x2 y[kParts][kPairs];
+#pragma unroll
+                        for (int w = 0; w < kParts; ++w)
+#pragma unroll
+                            for (int u = 0; u < kPairs; ++u)
+                                y[w][u] = load_coherent(
+                                    slot_of(g0 + (w0 + w < parts ? w0 + w : w0)) + at[u]);
+#pragma unroll
+                        for (int w = 0; w < kParts; ++w) {
+                            if (w0 + w >= parts) break;
+#pragma unroll
+                            for (int u = 0; u < kPairs; ++u) {
+                                const float f = factor[(w0 + w) * nr + x[u]];
+                                l[u] += share[(w0 + w) * nr + x[u]];
+                                if (f != 0.f) {
+                                    v[u][0] += f * y[w][u][0];
+                                    v[u][1] += f * y[w][u][1];
+                                }
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < kPairs; ++u)
+                        if (i0 + u * T::kThreads < items)
+                            finish_pair(i0 + u * T::kThreads, l[u], v[u]);
+                }
+            };
+            if (items > 2 * T::kThreads)
+                sums(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
+            else
+                sums(std::integral_constant<int, 1>(), std::integral_constant<int, 16>());
+        }
+    };
+
+    if (kWide && wave >= 4) __builtin_amdgcn_s_setprio(1);
+    begin();
+    int done = 0;  // tiles of the unit
+    for (int number = 0;; number = (number + 1) & (kSlots - 1)) {
+        step(number);
+        if (++done < n) continue;
+        finish();
+        cur += (uint64_t)n;
+        if (cur == end) break;
+        begin_next(next);
+        begin();
+        done = 0;
     }
+    wait_loads<0>();  // nothing of this workgroup may land in LDS after it ends
 }
 
-static int tile_wgs() { return kTileWgsPerCu * device_cu_count(); }
+static int tile_wgs(bool wide) { return device_cu_count() * (wide ? 1 : 2); }
+// Calls whose requests may have over 128 query rows of a key-value head (prompts)
+// take blocks of 256, eight waves of 32 rows against all keys of a tile: the keys
+// are read from L2 half as often. Others share a tile's keys out to the waves. One
+// kernel for both spilled its registers.
+static bool tile_wide(int max_rows, int Hq, int Hkv) {
+    return (int64_t)max_rows * (Hq / Hkv) > kNarrowRows;
+}
 static int tile_slot_rows(int max_rows, int Hq, int Hkv) {
     const int64_t m = (int64_t)max_rows * (Hq / Hkv);
-    return m >= kBlockRows ? kBlockRows : (int)((m + 31) / 32 * 32);
+    return m >= kWideRows ? kWideRows : (int)((m + 31) / 32 * 32);
 }
-static size_t tile_arrival_bytes() { return ((size_t)tile_wgs() * 4 + 255) & ~(size_t)255; }
+static size_t tile_arrival_bytes() { return ((size_t)tile_wgs(false) * 4 + 255) & ~(size_t)255; }
 
 size_t attention_ws_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
     (void)B;
     if (D != 64 && D != 128) return 256;
-    const size_t n = tile_arrival_bytes() +
-                     (size_t)2 * tile_wgs() *
+    const size_t n = kZeroBytes + tile_arrival_bytes() +
+                     (size_t)2 * tile_wgs(tile_wide(max_rows, Hq, Hkv)) *
                          (size_t)slot_floats(tile_slot_rows(max_rows, Hq, Hkv), D) * 4;
     return (n + 255) & ~(size_t)255;
 }
@@ -852,16 +1220,27 @@ template <int D, bool kE4m3>
 static hipError_t launch_tiles(const AttendParams &p, void *ws, hipStream_t s) {
     TileParams tp;
     tp.a = p;
-    tp.arrivals = static_cast<unsigned *>(ws);
-    tp.slots = reinterpret_cast<float *>(static_cast<char *>(ws) + tile_arrival_bytes());
+    char *at = static_cast<char *>(ws);
+    tp.zeros = at;
+    tp.arrivals = reinterpret_cast<unsigned *>(at + kZeroBytes);
+    tp.slots = reinterpret_cast<float *>(at + kZeroBytes + tile_arrival_bytes());
     tp.slot_rows = tile_slot_rows(p.max_rows, p.Hq, p.Hkv);
+    const int64_t item = kE4m3 ? 1 : 2;
+    tp.together = p.c.page % 16 == 0 && p.c.page_stride * item < (1ll << 32) &&
+                  p.c.slot_stride * item * p.c.page < (1ll << 32);
+    tp.page_bytes = (uint32_t)(p.c.page_stride * item);
+    tp.slot_bytes = (uint32_t)(p.c.slot_stride * item);
     for (int b = 0; b < p.B; b += kGroupRequests) {
         tp.a.B = p.B - b < kGroupRequests ? p.B - b : kGroupRequests;
         tp.a.cu = p.cu + b;
         tp.a.ctx = p.ctx + b;
         tp.a.c.table = p.c.table + (int64_t)b * p.c.table_width;
-        hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3>), dim3(tile_wgs()), dim3(kTileThreads), 0,
-                           s, tp);
+        if (tile_wide(p.max_rows, p.Hq, p.Hkv))
+            hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3, true>), dim3(tile_wgs(true)),
+                               dim3(Tiles<D, kE4m3, true>::kThreads), 0, s, tp);
+        else
+            hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3, false>), dim3(tile_wgs(false)),
+                               dim3(Tiles<D, kE4m3, false>::kThreads), 0, s, tp);
     }
     return hipGetLastError();
 }
