@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
 // Rows of one key-value head share its keys: with G query heads per key-value
 // head, a request's n rows are M = n*G query rows, taken in blocks of up to 256
 // against tiles of 64 to 256 positions (32 KiB of keys and values). A (head,
-// block) is a unit; the tiles of all units, laid end to end, are divided evenly
+// block) is a unit; the tiles of all units, laid end to end with a few places for each unit before them, are divided evenly
 // between the resident workgroups, so any mix of long and short requests fills
 // the chip, a single long context included, and no launch shape depends on the
 // lengths. A unit that ends up in several workgroups leaves partial results
@@ -153,7 +153,7 @@ constexpr int kNarrowRows = 128, kWideRows = 256;  // query rows of a block
 constexpr int kSlotBytes = 32768;                  // of a tile in LDS: keys, then values
 constexpr int kHalfSlot = kSlotBytes / 2;
 constexpr int kGroupRequests = 512;  // of one launch; larger batches take several
-constexpr int kMinTiles = 2;          // per workgroup: fewer would cost more to join than to read
+constexpr int kMinTiles = 2;  // per workgroup: fewer would cost more to join than to read
 constexpr int kZeroBytes = 256;       // of the workspace that stay zero
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -167,6 +167,21 @@ struct TileParams {
     bool together;
     uint32_t page_bytes, slot_bytes;
 };
+
+// The call's parameters, read again from the kernel's arguments: for what runs once
+// a unit or less. Kept from the start, they would push the scalars of every tile
+// out of the registers.
+__device__ __forceinline__ TileParams params_again() {
+    struct Words {
+        uint32_t w[sizeof(TileParams) / 4];
+    } words;
+    uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(TileParams) / 4; ++i)
+        words.w[i] = ((const __attribute__((address_space(4))) uint32_t *)at)[i];
+    return __builtin_bit_cast(TileParams, words);
+}
 
 // Floats of one partial result: (maximum, sum) and D values of each row.
 __host__ __device__ inline int64_t slot_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
@@ -283,6 +298,11 @@ struct Tiles {
     static constexpr int kThreads = kWaves * kWave;
     static constexpr int kSlots = kWide ? 4 : 2;         // tiles in LDS
     static constexpr int kBlockRows = kWide ? kWideRows : kNarrowRows;
+    // What a unit costs beside its tiles (its queries, its first tile, joining and
+    // storing its rows), in tiles: a unit has this many places, then its tiles. At 0,
+    // 1, 2, 3 and 5 the mixed batch took 377, 346, 315, 307 and 313 us, four prompts
+    // 378, 367, 350, 333 and 318 us.
+    static constexpr int kUnitTiles = kWide ? 5 : 3;
     static constexpr int kItem = kE4m3 ? 1 : 2;
     static constexpr int kRow = D * kItem;               // bytes
     static constexpr int kChunks = kRow / 16;            // of a row
@@ -382,13 +402,13 @@ struct Tiles {
         }
     }
     __device__ static __forceinline__ void enter(const TileParams &tp, Stager &g, const Unit &u) {
-        const PagedCache &c = tp.a.c;
+        const PagedCache c = params_again().a.c;
         g.base = static_cast<const char *>(wave_id() < kStagers ? c.k : c.v) +
                  (int64_t)u.head * c.head_stride * kItem;
         g.table = c.table + (int64_t)u.b * c.table_width;
     }
     __device__ static __forceinline__ void look_up(const TileParams &tp, Stager &g, int tile) {
-        const PagedCache &c = tp.a.c;
+        const PagedCache c = params_again().a.c;
         const int lane = threadIdx.x & (kWave - 1);
         g.batch0 = tile;
         if (!tp.together) return;
@@ -427,11 +447,12 @@ struct Tiles {
                     from[j] = base + (ok ? g.off[j] : (uint32_t)(lane & 15) * 16);
             }
         } else {
+            const TileParams cold = params_again();
 #pragma unroll
             for (int j = 0; j < kWaveLoads; ++j) {
                 const int r = j * kLoadRows + lane / kChunks;
-                const int64_t at = slot_offset(c, g.table, tile * kKeys + g.row0 + r, 0);
-                from[j] = at < 0 ? tp.zeros
+                const int64_t at = slot_offset(cold.a.c, g.table, tile * kKeys + g.row0 + r, 0);
+                from[j] = at < 0 ? cold.zeros
                                  : g.base + at * kItem +
                                        (((lane % kChunks) ^ swizzle<D, kE4m3>(r)) << 4);
             }
@@ -503,11 +524,12 @@ struct Tiles {
                                                    const AttendParams &p, const Task &t,
                                                    State &st, int lane) {
         const int h = lane >> 5;
+        const AttendParams cold = params_again().a;
 #pragma unroll 1
         for (int y = sub * 32; y < sub * 32 + 32; ++y) {
             if (!(bad[y / kWaveRows] >> (y % kWaveRows) & 1)) continue;
             const int key = tile * kKeys + y;
-            const int64_t at = slot_offset(p.c, t.table, key, 0);
+            const int64_t at = slot_offset(cold.c, t.table, key, 0);
             if (at < 0) continue;
             const bool see = visible(p, t, key);
 #pragma unroll
@@ -515,7 +537,7 @@ struct Tiles {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const float v = load1<kE4m3>(
-                        p.c.v, at + t.head_off + d * 32 + 8 * (r / 4) + 4 * h + (r & 3));
+                        cold.c.v, at + t.head_off + d * 32 + 8 * (r / 4) + 4 * h + (r & 3));
                     st.o[d][r] += see && !(fabsf(v) < INFINITY) ? v : 0.f;
                     __builtin_amdgcn_sched_barrier(0);  // one at a time: registers, not speed
                 }
@@ -689,8 +711,8 @@ struct Tiles {
             for (int i = 0; i < kSub; ++i) {
                 uint32_t no = 0;
                 if (t.hole)
-                    no = (uint32_t)__ballot(
-                        slot_offset(p.c, t.table, k0 + i * 32 + (lane & 31), 0) < 0);
+                    no = (uint32_t)__ballot(slot_offset(params_again().a.c, t.table,
+                                                        k0 + i * 32 + (lane & 31), 0) < 0);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int y = 8 * (r / 4) + 4 * h + (r & 3);
@@ -745,6 +767,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     using Unit = typename T::Unit;
     constexpr int kBlockRows = T::kBlockRows, kSlots = T::kSlots, kWaveLoads = T::kWaveLoads;
     constexpr int kTileThreads = T::kThreads, kTileWaves = T::kWaves;
+    constexpr int kUnitTiles = T::kUnitTiles;
     __shared__ typename T::Lds s;
     __shared__ __attribute__((aligned(1024))) char slot0[kSlotBytes];
     __shared__ __attribute__((aligned(1024))) char slot1[kSlotBytes];
@@ -755,18 +778,18 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = T::wave_id();
     const int G = p.Hq / p.Hkv, wgs = gridDim.x;
 
-    // tiles before every request
+    // places before every request
     if (tid == 0) s.before[0] = 0;
     if ((int64_t)p.max_rows * G <= kBlockRows) {
         for (int b = tid; b < p.B; b += kTileThreads) {
             const Request q = load_request<kBlockRows>(p, b);
-            s.before[b + 1] = q.M > 0 ? (uint64_t)block_of<kBlockRows, T::kKeys>(p, q, 0).tiles * p.Hkv : 0;
+            s.before[b + 1] = q.M > 0 ? (uint64_t)(kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, 0).tiles) * p.Hkv : 0;
         }
     } else {
         for (int b = wave; b < p.B; b += kTileWaves) {
             const Request q = load_request<kBlockRows>(p, b);
             uint64_t n = 0;
-            for (int i = lane; i < q.blocks; i += kWave) n += block_of<kBlockRows, T::kKeys>(p, q, i).tiles;
+            for (int i = lane; i < q.blocks; i += kWave) n += kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, i).tiles;
             n = wave_incl_sum_u64(n);
             if (lane == kWave - 1) s.before[b + 1] = n * p.Hkv;
         }
@@ -796,7 +819,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     __syncthreads();
     const uint64_t total = s.before[p.B];
     uint64_t per = (uint64_t)udiv64((int64_t)total + wgs - 1, wgs);
-    per = per < kMinTiles ? kMinTiles : per;
+    per = per < kMinTiles + kUnitTiles ? kMinTiles + kUnitTiles : per;  // so one tile at least
     // Workgroups go to the 8 XCDs in turn: each XCD takes one run of the tiles, so
     // that units of one head meet in one L2.
     const int used = (int)udiv64((int64_t)(total + per - 1), (int64_t)per);
@@ -807,8 +830,9 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     const uint64_t start = (uint64_t)g * per;
     const uint64_t end = start + per < total ? start + per : total;
 
-    // the unit of the first tile
+    // the unit of the first place, and the first tile at or after it
     Unit next;
+    uint64_t cur = start;
     {
         int b = 0, hi = p.B - 1;
         while (b < hi) {
@@ -824,7 +848,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         int blk = 0;
         for (int i0 = 0; q.blocks > 1; i0 += kWave) {
             const int i = i0 + lane;
-            const uint64_t n = i < q.blocks ? (uint64_t)block_of<kBlockRows, T::kKeys>(p, q, i).tiles : 0;
+            const uint64_t n =
+                i < q.blocks ? (uint64_t)kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, i).tiles : 0;
             const uint64_t in64 = wave_incl_sum_u64(n);
             const uint64_t all = __shfl(in64, kWave - 1, kWave);
             if (rest < all || i0 + kWave >= q.blocks) {
@@ -841,10 +866,16 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         next.blk = __builtin_amdgcn_readfirstlane(blk);
         next.q = scalar_request<kBlockRows>(p, next.b);
         next.k = block_of<kBlockRows, T::kKeys>(p, next.q, next.blk);
-        next.tile = next.k.tile + __builtin_amdgcn_readfirstlane((int)rest);
+        int place = __builtin_amdgcn_readfirstlane((int)rest) - kUnitTiles;
+        if (place < 0) {
+            cur -= (int64_t)place;
+            place = 0;
+        }
+        next.tile = next.k.tile + place;
         next.left = next.k.tiles - (next.tile - next.k.tile);
     }
     auto begin_next = [&](Unit &u) {
+        const AttendParams p = params_again().a;
         if (++u.blk == u.q.blocks) {
             u.blk = 0;
             if (++u.head == p.Hkv) {
@@ -860,8 +891,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
 
     // The stager runs three tiles ahead; past the last one it repeats it, so that
     // a fixed number of loads is always on its way.
-    const int count = (int)(end - start);
-    int staged = 0;
+    int64_t left = (int64_t)(end - cur);  // places from the tile to stage to the end
     typename T::Stager sg;
     T::stager(tp, sg);
     Unit ahead = next;
@@ -869,7 +899,9 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     T::look_up(tp, sg, ahead.tile);
     auto stage = [&](int number, int lane) {
         T::issue(tp, sg, ahead.tile, slots, number, lane);
-        if (++staged < count) {
+        const int step = ahead.left > 1 ? 1 : 1 + kUnitTiles;
+        if (left > step) {
+            left -= step;
             if (--ahead.left == 0) {
                 begin_next(ahead);
                 T::enter(tp, sg, ahead);
@@ -884,7 +916,6 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
 
     typename T::Task t;
     typename T::State st;
-    uint64_t cur = start;  // the unit's first tile here
     int n = 0, rows = 0, qts = 1, kgs = 1, qt = 0, kg = 0, m = 0, hq = 0;
     int each = 1;  // times 32 keys of a tile for every group of waves
     int64_t row = 0;
@@ -903,7 +934,9 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         asm volatile("" ::: "memory");  // no access to LDS is moved across the barrier
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        stage((number + kSlots - 1) & (kSlots - 1), lane);
+        // Where three tiles are on their way the next loads wait for this tile's
+        // products: issued by all waves at once they hold the waves up.
+        if (!kWide) stage((number + kSlots - 1) & (kSlots - 1), lane);
         if (t.active) {
             if constexpr (kWide) {
 #pragma unroll 1
@@ -926,10 +959,13 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 }
             }
         }
+        if (kWide) stage((number + kSlots - 1) & (kSlots - 1), lane);
         ++next.tile;
     };
 
     auto begin = [&]() {
+        const AttendParams p = params_again().a;
+        const int G = p.Hq / p.Hkv;
         const int m0 = next.blk * kBlockRows;
         rows = next.q.M - m0 < kBlockRows ? next.q.M - m0 : kBlockRows;
         const uint64_t rest = end - cur;
@@ -994,6 +1030,9 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     // the unit's tiles here are done: joins the waves, stores the rows or leaves
     // them for the last workgroup
     auto finish = [&]() {
+        const TileParams tp = params_again();
+        const AttendParams &p = tp.a;
+        const int G = p.Hq / p.Hkv;
         st.l = half_sum(st.l);
         // the groups of keys meet, 32 elements of all rows at a time
         for (int half = kWide ? 0 : kgs / 2; half >= 1; half /= 2) {
@@ -1177,15 +1216,14 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         }
     };
 
-    if (kWide && wave >= 4) __builtin_amdgcn_s_setprio(1);
     begin();
     int done = 0;  // tiles of the unit
     for (int number = 0;; number = (number + 1) & (kSlots - 1)) {
         step(number);
         if (++done < n) continue;
         finish();
-        cur += (uint64_t)n;
-        if (cur == end) break;
+        cur += (uint64_t)(n + kUnitTiles);
+        if (cur >= end) break;
         begin_next(next);
         begin();
         done = 0;
