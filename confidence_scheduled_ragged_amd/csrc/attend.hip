@@ -643,6 +643,24 @@ struct Tiles {
                          (uint32_t)x[2 * d + 1][1]};
         return __builtin_bit_cast(bf16x8, y);
     }
+    // The same, one operand at a time, for the scheduler to place: where the loads
+    // into LDS run three tiles ahead, the last of them were issued a tile ago.
+    __device__ static __forceinline__ bf16x8 value_at(const ValueAddresses &v, int kk, int d) {
+        if constexpr (kE4m3) {
+            const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (__attribute__((address_space(3))) i32x2 *)(uintptr_t)(v.at[d] + 16 * kk * kRow));
+            return widen((uint32_t)x[0], (uint32_t)x[1]);
+        } else {
+            s16x4 x[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(v.at[2 * d + e] +
+                                                                           16 * kk * kRow));
+            return __builtin_bit_cast(bf16x8,
+                                      __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
     template <int kSub, int kk>
     __device__ static __forceinline__ void add_values(const ValueAddresses &v, const bf16x8 *w,
                                                       State &st) {
@@ -686,11 +704,11 @@ struct Tiles {
         for (int i = 0; i < kSub; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[i][r] = 0.f;
+        // four operands are on their way from LDS behind the product at work
+        constexpr int kAhead = 4, kProducts = D / 16 * kSub;
+        bf16x8 a[kAhead];
         slots.pick(number, [&](const char *slot) {
             const char *kb = slot + sub * 32 * kRow;
-            // four operands are on their way from LDS behind the product at work
-            constexpr int kAhead = 4, kProducts = D / 16 * kSub;
-            bf16x8 a[kAhead];
             auto read = [&](int u) {
                 a[u % kAhead] = keys_of(kb + u % kSub * 32 * kRow, u / kSub, lane);
             };
@@ -740,6 +758,15 @@ struct Tiles {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) st.o[d][r] *= keep;
         }
+        const ValueAddresses v =
+            value_addresses(slots.address(number) + kHalfSlot + sub * 32 * kRow, lane);
+        // the first values are read behind the exponentials
+        constexpr int kVectorCrosses = 0x2 | 0x4;  // vector and scalar instructions
+        if constexpr (kWide) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) a[u] = value_at(v, u / (D / 32), u % (D / 32));
+            __builtin_amdgcn_sched_barrier(kVectorCrosses);
+        }
         const float m = st.m == -INFINITY ? 0.f : st.m;
         float sum = 0.f;
         bf16x8 w[kSub * 2];
@@ -756,8 +783,19 @@ struct Tiles {
             }
         }
         st.l += sum;
-        add_values<kSub, 0>(
-            value_addresses(slots.address(number) + kHalfSlot + sub * 32 * kRow, lane), w, st);
+        if constexpr (kWide) {
+#pragma unroll
+            for (int u = 0; u < kProducts; ++u) {
+                const int kk = u / (D / 32), d = u % (D / 32);
+                st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[u % kAhead], w[kk], st.o[d], 0,
+                                                                  0, 0);
+                if (u + kAhead < kProducts)
+                    a[u % kAhead] = value_at(v, (u + kAhead) / (D / 32), (u + kAhead) % (D / 32));
+                __builtin_amdgcn_sched_barrier(kVectorCrosses);
+            }
+        } else {
+            add_values<kSub, 0>(v, w, st);
+        }
     }
 };
 
