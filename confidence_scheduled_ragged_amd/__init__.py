@@ -89,6 +89,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> torch.Tensor:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t
+    # what of it is wrong
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -104,6 +108,11 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> torch.T
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream's handle without a Stream object in between."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ok(fn: str, status: int):
@@ -531,14 +540,14 @@ _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 def _paged(k_cache, v_cache, cu_seqlens, ctx_lens, block_table):
     """Checks the paged cache and the packed batch's lengths; returns B, the
     cache's type, sizes and strides."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape, [pages, Hkv, page_size, D]")
-    if k_cache.device.type != "cuda" or v_cache.device != k_cache.device:
+    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.get_device() != k_cache.get_device():
         raise ValueError(f"the caches must be on one GPU (got {k_cache.device}, {v_cache.device})")
-    if k_cache.dtype not in _CACHE_TYPES or v_cache.dtype != k_cache.dtype:
-        raise TypeError(f"the caches must be bfloat16 or float8_e4m3fn (got {k_cache.dtype}, "
+    if dtype not in _CACHE_TYPES or v_cache.dtype is not dtype:
+        raise TypeError(f"the caches must be bfloat16 or float8_e4m3fn (got {dtype}, "
                         f"{v_cache.dtype})")
-    strides = k_cache.stride()
     if v_cache.stride() != strides or strides[3] != 1:
         raise ValueError("k_cache and v_cache must share strides, with D contiguous")
     B = cu_seqlens.numel() - 1
@@ -547,20 +556,21 @@ def _paged(k_cache, v_cache, cu_seqlens, ctx_lens, block_table):
     _need(block_table, "block_table", torch.int32)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, pages of a request)")
-    return B, _CACHE_TYPES[k_cache.dtype], k_cache.shape, strides
+    return B, _CACHE_TYPES[dtype], shape, strides
 
 
 def _packed_heads(t, name, rows, heads, D):
-    """Checks packed [rows, heads, D] bf16 with rows at any stride."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    """Checks packed [rows, heads, D] bf16 with rows at any stride; returns its strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16} (got {t.dtype})")
-    if tuple(t.shape) != (rows, heads, D):
+    if t.shape != (rows, heads, D):
         raise ValueError(f"{name} must have shape {(rows, heads, D)} (got {tuple(t.shape)})")
-    if t.stride(2) != 1:
+    strides = t.stride()
+    if strides[2] != 1:
         raise ValueError(f"{name} must have its last axis contiguous")
-    return t
+    return strides
 
 
 def dspark_append_kv(q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cache, v_cache,
@@ -574,25 +584,27 @@ def dspark_append_kv(q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cac
     B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(k_cache, v_cache, cu_seqlens,
                                                              ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
-    _packed_heads(q, "q", rows, Hq, D)
-    _packed_heads(k, "k", rows, Hkv, D)
-    _packed_heads(v, "v", rows, Hkv, D)
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        if t.stride(1) != D and t.shape[1] > 1:
-            raise ValueError(f"{n} must have its heads side by side")
+    qs = _packed_heads(q, "q", rows, Hq, D)
+    ks = _packed_heads(k, "k", rows, Hkv, D)
+    vs = _packed_heads(v, "v", rows, Hkv, D)
+    if (qs[1] != D and Hq > 1) or ((ks[1] != D or vs[1] != D) and Hkv > 1):
+        raise ValueError("q, k and v must have their heads side by side")
     _need(cos, "cos", torch.float32)
-    _need(sin, "sin", torch.float32, cos.shape)
-    if cos.dim() != 2:
+    angles = cos.shape
+    _need(sin, "sin", torch.float32, angles)
+    if len(angles) != 2:
         raise ValueError("cos must have shape (positions, rotated pairs)")
-    dev = q.device
-    out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
+    if out is None:
+        out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, (rows, Hq, D))
-    _ok("dspark_append_kv", lib().dspark_append_kv(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0), k.stride(0), v.stride(0),
-        cos.data_ptr(), sin.data_ptr(), cos.shape[0], cos.shape[1], 1 if interleaved else 0,
-        cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, rows, Hq, Hkv, D, k_cache.data_ptr(),
-        v_cache.data_ptr(), kind, pages, page, ps, hs, ss, k_scale, v_scale,
-        block_table.data_ptr(), block_table.shape[1], out.data_ptr(), _stream(dev)))
+    status = lib().dspark_append_kv(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], ks[0], vs[0], cos.data_ptr(),
+        sin.data_ptr(), angles[0], angles[1], 1 if interleaved else 0, cu_seqlens.data_ptr(),
+        ctx_lens.data_ptr(), B, rows, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), kind,
+        pages, page, ps, hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
+        out.data_ptr(), _raw_stream(q.get_device()))
+    if status:
+        _ok("dspark_append_kv", status)
     return out
 
 
@@ -600,23 +612,24 @@ def dspark_attention_workspace_bytes(B: int, max_rows: int, Hq: int, Hkv: int, D
     return int(lib().dspark_attention_workspace_bytes(B, max_rows, Hq, Hkv, D))
 
 
-_ATTN_WS: Dict[tuple, torch.Tensor] = {}
+_ATTN_WS: Dict[int, list] = {}
 
 
 def attention_workspace(B: int, max_rows: int, Hq: int, Hkv: int, D: int, device) -> torch.Tensor:
     """A zero-initialised workspace of dspark_verify_attention, cached per
-    device. Calls sharing it must not overlap in time."""
-    device = torch.device(device)
-    need = dspark_attention_workspace_bytes(B, max_rows, Hq, Hkv, D)
+    device. Calls sharing it must not overlap in time (one stream, or ordered).
+    One that has become too small stays allocated: a captured graph may use it."""
+    need = lib().dspark_attention_workspace_bytes(B, max_rows, Hq, Hkv, D)
     if need == 0:
         raise ValueError(f"invalid sizes B={B} max_rows={max_rows} Hq={Hq} Hkv={Hkv} D={D}")
-    key = _ws_key(device)
-    ws = _ATTN_WS.get(key)
-    if ws is None or ws.numel() < need:
+    device = device if isinstance(device, torch.device) else torch.device(device)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    held = _ATTN_WS.setdefault(index, [])
+    if not held or held[-1].numel() < need:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         dspark_workspace_init(ws)
-        _ATTN_WS[key] = ws
-    return ws
+        held.append(ws)
+    return held[-1]
 
 
 def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, max_rows,
@@ -630,21 +643,23 @@ def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_tab
     B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(k_cache, v_cache, cu_seqlens,
                                                              ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
-    _packed_heads(q, "q", rows, Hq, D)
-    dev = q.device
-    out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
+    qs = _packed_heads(q, "q", rows, Hq, D)
+    if out is None:
+        out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, (rows, Hq, D))
     max_rows = min(int(max_rows), rows)
     if ws is None:
-        ws = attention_workspace(B, max_rows, Hq, Hkv, D, dev)
+        ws = attention_workspace(B, max_rows, Hq, Hkv, D, q.device)
     else:
         _need(ws, "ws", torch.uint8)
-    _ok("dspark_verify_attention", lib().dspark_verify_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), kind,
-        pages, page, ps, hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
+    status = lib().dspark_verify_attention(
+        q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), kind, pages, page, ps,
+        hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
         cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, rows, max_rows, Hq, Hkv, D, int(window),
         D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream(dev)))
+        _raw_stream(q.get_device()))
+    if status:
+        _ok("dspark_verify_attention", status)
     return out
 
 
@@ -683,10 +698,14 @@ def dspark_sample_accept(logits, packed_src_row, cu_seqlens, tokens, uniforms, t
     _need(acc, "accepted", torch.int32, (B,))
     _need(bon, "bonus", torch.int32, (B,))
     ws = workspace(B, g1 - 1, V, dev) if ws is None else _need(ws, "ws", torch.uint8)
-    _ok("dspark_sample_accept", lib().dspark_sample_accept(
-        _ptr(logits), _ptr(packed_src_row), _ptr(cu_seqlens), _ptr(tokens), _ptr(uniforms),
-        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), B, g1 - 1, V, _ptr(smp),
-        _ptr(acc), _ptr(bon), _ptr(ws), ws.numel(), _stream(dev)))
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    status = lib().dspark_sample_accept(
+        logits.data_ptr(), at(packed_src_row), cu_seqlens.data_ptr(), tokens.data_ptr(),
+        uniforms.data_ptr(), at(temperature), at(top_k), at(top_p), at(min_p), B, g1 - 1, V,
+        smp.data_ptr(), acc.data_ptr(), bon.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(tokens.get_device()))
+    if status:
+        _ok("dspark_sample_accept", status)
     return smp, acc, bon
 
 
