@@ -153,3 +153,40 @@ def test_on_another_stream():
     with torch.cuda.stream(side):
         check(c)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_pool_past_32_bits(cache):
+    """The last pages of pools of over 2^32 bytes."""
+    Hq, Hkv, D, page = 4, 2, 128, 16
+    item = 1 if cache == "e4m3" else 2
+    dtype = torch.float8_e4m3fn if cache == "e4m3" else torch.bfloat16
+    pages = 5 * 2 ** 30 // (Hkv * page * D * item)
+    gen = torch.Generator().manual_seed(7)
+    x = torch.randn((3, Hq + 2 * Hkv, D), generator=gen).bfloat16()
+    q, k, v = x.split((Hq, Hkv, Hkv), 1)
+    angle = torch.rand((40, D // 2), generator=gen) * 6
+    cos, sin = angle.cos(), angle.sin()
+    cu, ctx = [0, 3], [30]
+    small = torch.zeros((4, Hkv, page, D)).to(dtype)
+    table = torch.tensor([[0, 2, 3]], dtype=torch.int32)
+    out = torch.zeros((3, Hq, D)).bfloat16()
+    scale = dict(k_scale=0.01, v_scale=0.02) if item == 1 else {}
+    O, K, V, ot, kt, vt = ref.append(q, k, v, cos, sin, cu, ctx, table, small, small, out=out,
+                                     **scale)
+    pools = [torch.empty((pages, Hkv, page, D), dtype=torch.uint8 if item == 1 else dtype,
+                         device=DEV) for _ in range(2)]
+    for p in pools:
+        p[pages - 4:] = 0
+    kc, vc = (p.view(dtype) for p in pools)
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device=DEV)  # noqa: E731
+    got = dspark.dspark_append_kv(*(t.to(DEV) for t in (x[:, :Hq], x[:, Hq:Hq + Hkv],
+                                                        x[:, Hq + Hkv:])),
+                                  cos.to(DEV), sin.to(DEV), i32(cu), i32(ctx),
+                                  (table + pages - 4).to(DEV), kc, vc, **scale)
+    torch.cuda.synchronize()
+    ends = [p[pages - 4:].cpu().view(dtype).double() for p in pools]
+    del pools, kc, vc
+    assert bool(((got.cpu().double() - O).abs() <= ot).all())
+    assert bool(((ends[0] - K).abs() <= kt).all()) and bool(((ends[1] - V).abs() <= vt).all())
+    torch.cuda.empty_cache()

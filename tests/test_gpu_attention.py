@@ -273,3 +273,73 @@ def test_infinities_that_a_window_has_left_behind(D):
         r0, n = c["cu"][b], c["cu"][b + 1] - c["cu"][b]
         assert torch.equal(got[r0 + first:r0 + n], clean[r0 + first:r0 + n])
         assert not bool(got[r0 + (0 if b == 0 else 3):r0 + first].isfinite().any())
+
+
+def test_more_requests_than_one_launch_takes():
+    rng = random.Random(14)
+    rows = [rng.choice((0, 1, 1, 2, 3)) for _ in range(1100)]
+    ctx = [rng.randint(0, 40) for _ in rows]
+    check(make(rows, ctx, 2, 1, 64, 16, seed=14))
+
+
+@pytest.mark.parametrize("page", [7, 16, 24])
+@pytest.mark.parametrize("D,cache", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3")])
+def test_blocks_of_many_rows(page, D, cache):
+    """Requests of several blocks of 256 rows among short ones, on what is cached."""
+    check(make([300, 2, 0, 65, 33], [70, 500, 9, 0, 31], 4, 2, D, page, cache, seed=15),
+          **SCALES[cache])
+
+
+@pytest.mark.parametrize("D,cache", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3")])
+@pytest.mark.parametrize("n", [8, 9, 16, 17, 32, 33])
+def test_rows_around_the_waves_of_a_block(D, cache, n):
+    """G = 4: 32, 64 and 128 rows of a key-value head, and four more of each."""
+    check(make([n, 1, n], [100, 0, 700], 4, 1, D, 16, cache, seed=n), **SCALES[cache])
+
+
+def test_windows_over_prompts_and_holes():
+    c = make([200, 150], [20, 400], 4, 2, 128, 16, seed=16)
+    c["table"][0, 3] = -1
+    c["table"][1, 25:28] = -1
+    check(c, window=70)
+    check(c)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [3, 150])
+def test_a_pool_past_32_bits(cache, n):
+    """Pages whose bytes lie past 2^32, the table naming the last ones of the pool."""
+    c = make([n, 1], [200, 40], 4, 2, 128, 16, cache, seed=17)
+    item = 1 if cache == "e4m3" else 2
+    used, shape = c["kc"].shape[0], c["kc"].shape
+    pages = 5 * 2 ** 30 // (2 * 16 * 128 * item)
+    big = []
+    for x in (c["kc"], c["vc"]):
+        p = torch.empty((pages,) + shape[1:], dtype=torch.uint8 if item == 1 else x.dtype,
+                        device=DEV)
+        p[pages - used:] = x.view(p.dtype).to(DEV) if item == 1 else x.to(DEV)
+        big.append(p.view(x.dtype))
+    out = torch.zeros((c["cap"], 4, 128), dtype=torch.bfloat16)
+    want, tol = ref.attend(c["q"], c["kc"], c["vc"], c["cu"], c["ctx"], c["table"], c["max_rows"],
+                           out=out, **SCALES[cache])
+    c["table"] = torch.where(c["table"] >= 0, c["table"] + pages - used, c["table"])
+    got = call(c, *big, out.to(DEV), **SCALES[cache])
+    torch.cuda.synchronize()
+    del big
+    assert bool(((got.cpu().double() - want).abs() <= tol).all())
+    torch.cuda.empty_cache()
+
+
+def test_a_scale_of_either_sign():
+    c = make([5, 40], [100, 10], 4, 2, 128, 16, seed=18)
+    check(c, scale=-0.05)
+    check(make([5, 40], [100, 10], 4, 2, 64, 16, seed=18), scale=-1e-3)
+
+
+def test_a_smaller_call_after_a_larger_one_and_back():
+    """Workspaces are shared by calls of all sizes, narrow and wide."""
+    big = make([300, 40], [500, 4000], 8, 2, 128, 16, seed=19)
+    small = make([1, 1], [6000, 3], 8, 2, 64, 16, seed=20)
+    for _ in range(3):
+        check(small)
+        check(big)
