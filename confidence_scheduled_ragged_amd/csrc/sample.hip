@@ -575,6 +575,40 @@ __device__ __forceinline__ Drawn draw_wide(SampleLds &s, const Row &row, const D
     });
 }
 
+// The request that owns packed row r: the first whose end lies past it (B if
+// none does), so that rows have one owner each whatever cu holds. `below` is this
+// lane's largest end of an earlier request: the wave's largest is where the
+// owner's rows start.
+__device__ __forceinline__ int wave_owner_of(const int32_t *__restrict__ cu, int B, int r,
+                                             int &below) {
+    const int lane = threadIdx.x & (kWave - 1);
+    below = 0;
+    for (int i0 = 0; i0 < B; i0 += 4 * kWave) {
+        int x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kWave + lane;
+            x[u] = i < B ? cu[i + 1] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint64_t m = __ballot(x[u] > r);
+            const int first = m ? __ffsll((unsigned long long)m) - 1 : kWave;
+            if (lane < first && x[u] > below) below = x[u];
+            if (m) return i0 + u * kWave + first;
+        }
+    }
+    return B;
+}
+__device__ __forceinline__ int wave_max_int(int x) {
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) {
+        const int y = __shfl_xor(x, off, kWave);
+        x = y > x ? y : x;
+    }
+    return x;
+}
+
 // One workgroup per packed row.
 __global__ __launch_bounds__(kSampleThreads, kSampleWavesPerSimd) void sample_rows_kernel(SampleParams p,
                                                                      uint64_t *arrivals) {
@@ -585,14 +619,24 @@ __global__ __launch_bounds__(kSampleThreads, kSampleWavesPerSimd) void sample_ro
     const int r = blockIdx.x;
     const int src = p.psrc ? p.psrc[r] : r;
     const int total = packed_total(p.cu, p.B, cap);
-    if (arrivals && r < p.B && p.cu[r + 1] <= p.cu[r] && tid == 0) {  // a request without rows
-        p.acc[r] = 0;
-        p.bonus[r] = -1;
+    // accepted and bonus of request r, if it has no rows; by one wave
+    auto settle_empty = [&]() {
+        int start = 0;
+        for (int i = lane; i <= r; i += kWave) start = p.cu[i] > start ? p.cu[i] : start;
+        start = wave_max_int(start);
+        if (lane == 0 && (p.cu[r + 1] <= start || start >= total)) {
+            p.acc[r] = 0;
+            p.bonus[r] = -1;
+        }
+    };
+    if (r >= total) {
+        if (arrivals && r < p.B && wave == 0) settle_empty();
+        return;
     }
-    if (r >= total) return;
     const bool exists = src >= 0 && src < cap;
     const Row row(p.logits + (int64_t)(exists ? src : 0) * p.V, exists ? p.V : 0);
-    const int b = wave_request_of(p.cu, p.B, r);
+    int below;
+    const int b = wave_owner_of(p.cu, p.B, r, below);
     Draw d;
     const bool owned = b < p.B && r >= p.cu[0];
     d.T = owned && p.temperature ? (double)p.temperature[b] : 1.0;
@@ -714,17 +758,16 @@ __global__ __launch_bounds__(kSampleThreads, kSampleWavesPerSimd) void sample_ro
         if (out.j < 0) chosen = 0;
         else chosen = out.bits ? index_of<false>(s, row, out) : index_of<true>(s, row, out);
     }
-    if (!owned) return;
+    if (arrivals && r < p.B && wave == 1) settle_empty();
+    if (!owned || wave != 0) return;
     if (!arrivals) {
-        if (tid == 0) p.sample[r] = chosen;
+        if (lane == 0) p.sample[r] = chosen;
         return;
     }
     // the last row of a request to arrive accepts its drafts
-    if (wave != 0) return;
-    int start = p.cu[b], end = p.cu[b + 1];
-    start = start < 0 ? 0 : (start > total ? total : start);
-    end = end < start ? start : (end > total ? total : end);
-    const int n = end - start;
+    below = below > p.cu[0] ? below : p.cu[0];
+    const int start = wave_max_int(below);
+    const int end = p.cu[b + 1] < total ? p.cu[b + 1] : total, n = end - start;
     bool last = false;
     if (lane == 0) {
         __hip_atomic_store(p.sample + r, chosen, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

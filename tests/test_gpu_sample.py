@@ -311,3 +311,21 @@ def test_a_masked_vocabulary_over_16_bits():
         keep[:, 5] = True
         fill(c, mask, ~keep)
         check(c)
+
+
+def test_lengths_out_of_order_leave_the_workspace_as_it_was():
+    """cu_seqlens that go down give every row one owner; the next call is right."""
+    c = make(40, 4, 700, seed=55)
+    good = c["cu"]
+    ws = torch.zeros(dspark.dspark_workspace_bytes(40, 4, 700), dtype=torch.uint8, device=DEV)
+    rng = np.random.default_rng(56)
+    for _ in range(4):
+        c["cu"] = rng.integers(-3, 205, 41)
+        call(c, ws=ws)
+        torch.cuda.synchronize()
+    c["cu"] = good
+    want = ref.sample_accept(c["logits"].double().numpy(), c["psrc"], c["cu"], c["tokens"],
+                             c["uniforms"], c["temperature"], c["top_k"], c["top_p"], c["min_p"])
+    for g, w in zip(call(c, ws=ws), want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    assert int(ws.sum()) == 0
