@@ -44,8 +44,11 @@ __device__ __forceinline__ float load1(const void *pool, int64_t at) {
     return bf16_f32(static_cast<const uint16_t *>(pool)[at]);
 }
 
-// One wave per (packed row, query head): 64 keys at a time, a lane per key for
-// the scores and a lane per output element for the weighted values.
+// Any head size and alignment: one wave per (packed row, query head), 64 keys at a
+// time, a lane per key for the scores and a lane per output element for the
+// weighted values. Bound by its latency: 32 requests of mixed traffic at D = 96 took
+// 2127 us here and take 66 us in the tiles below, so only heads over 128 and pools
+// that 16-byte loads do not fit come here.
 template <bool kE4m3>
 __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p) {
     __shared__ float q_s[kMaxHeadDim];
@@ -118,20 +121,28 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
 // ---------------------------------------------------------------- tiled kernel
 //
 // Rows of one key-value head share its keys: with G query heads per key-value
-// head, a request's n rows are M = n*G query rows, taken in blocks of up to 256
-// against tiles of 64 to 256 positions (32 KiB of keys and values). A (head,
-// block) is a unit; the tiles of all units, laid end to end with a few places for each unit before them, are divided evenly
-// between the resident workgroups, so any mix of long and short requests fills
-// the chip, a single long context included, and no launch shape depends on the
-// lengths. A unit that ends up in several workgroups leaves partial results
-// (maximum, sum, weighted values) in the workspace, and the last workgroup to
-// arrive joins them in tile order.
+// head, a request's n rows are M = n*G query rows, taken in blocks of up to 128 or
+// 256 against tiles of 64 to 256 positions (32 KiB of keys and values). A (head,
+// block) is a unit; the tiles of all units, laid end to end with a few places
+// ahead of each unit's for what it costs beside them, are divided evenly between
+// the resident workgroups, so any mix of long and short requests fills the chip, a
+// single long context included, and no launch shape depends on the lengths. A unit
+// that ends up in several workgroups leaves partial results (maximum, sum, weighted
+// values) in the workspace, and the last workgroup to arrive joins them in tile
+// order.
 //
-// One workgroup of eight waves a CU holds four tiles in LDS: one in use, three
-// on their way, loaded straight into LDS without passing registers, whatever
-// unit they belong to. Ordinary batches are bound by HBM, and 96 KiB a CU in
-// flight is what keeps it busy: with one tile ahead, through registers, and two
-// workgroups a CU the loads alone took 326 of the 409 us of the mixed batch.
+// Tiles are loaded from the pages straight into LDS, ahead of the tile at work and
+// whatever unit they belong to. Through registers, the loads alone took 326 of the
+// 409 us of a mixed batch (256 requests, 1.33 GB of keys and values) and 405 of the
+// 831 us of a prompt's chunk (2048 rows on 14000 positions). Calls of up to 128 query
+// rows a head (decoding, verify windows) are bound by HBM: two workgroups of four
+// waves a CU, a tile at work and one on its way in each. The mixed batch takes 297
+// us, 4.5 TB/s; four contexts of 40000 to 120000 in 8 bits 143 us, 4.5 TB/s; one
+// token at 4000, bound by a chain of some ten round trips to memory, 21 us. Calls
+// with more (prompts) are bound by the matrix and vector instructions of the
+// softmax, which two waves of a SIMD overlap poorly: one workgroup of eight waves a
+// CU, four tiles in LDS, so that keys are read from L2 once for 256 rows. The chunk
+// takes 592 us, 851 TFLOP/s; four prompts of 1882 to 2902 tokens 312 us, 671 TFLOP/s.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds 16 of a query's 32
 // scores of one MFMA (the other 16 sit in lane ^ 32), so the softmax needs one
@@ -292,7 +303,9 @@ __device__ __forceinline__ int swizzle(int r) {
     return (r >> 2) & 3;
 }
 
-template <int D, bool kE4m3, bool kWide>
+// D is the head size that the tiles are made for; with kPadded the heads are
+// shorter, and the elements between come from the zeros.
+template <int D, bool kE4m3, bool kWide, bool kPadded>
 struct Tiles {
     static constexpr int kWaves = kWide ? 8 : 4;
     static constexpr int kThreads = kWaves * kWave;
@@ -390,6 +403,10 @@ struct Tiles {
         int batch[kEntries];
         int batch0;
     };
+    // The chunk of its row that a lane fetches in load j.
+    __device__ static __forceinline__ int chunk_of(int lane, int j) {
+        return (lane % kChunks) ^ swizzle<D, kE4m3>(j * kLoadRows + lane / kChunks);
+    }
     __device__ static __forceinline__ void stager(const TileParams &tp, Stager &g) {
         const PagedCache &c = tp.a.c;
         const int lane = threadIdx.x & (kWave - 1), w = wave_id();
@@ -397,8 +414,7 @@ struct Tiles {
 #pragma unroll
         for (int j = 0; j < kWaveLoads; ++j) {
             const int r = j * kLoadRows + lane / kChunks;
-            g.off[j] = (uint32_t)(r % 16) * tp.slot_bytes +
-                       (((lane % kChunks) ^ swizzle<D, kE4m3>(r)) << 4);
+            g.off[j] = (uint32_t)(r % 16) * tp.slot_bytes + (chunk_of(lane, j) << 4);
         }
     }
     __device__ static __forceinline__ void enter(const TileParams &tp, Stager &g, const Unit &u) {
@@ -446,15 +462,21 @@ struct Tiles {
                 for (int j = e * kWaveLoads / kEntries; j < (e + 1) * kWaveLoads / kEntries; ++j)
                     from[j] = base + (ok ? g.off[j] : (uint32_t)(lane & 15) * 16);
             }
+            if constexpr (kPadded) {
+#pragma unroll
+                for (int j = 0; j < kWaveLoads; ++j)
+                    if (chunk_of(lane, j) * 16 >= tp.a.D * kItem)
+                        from[j] = tp.zeros + (lane & 15) * 16;
+            }
         } else {
             const TileParams cold = params_again();
 #pragma unroll
             for (int j = 0; j < kWaveLoads; ++j) {
                 const int r = j * kLoadRows + lane / kChunks;
                 const int64_t at = slot_offset(cold.a.c, g.table, tile * kKeys + g.row0 + r, 0);
-                from[j] = at < 0 ? cold.zeros
-                                 : g.base + at * kItem +
-                                       (((lane % kChunks) ^ swizzle<D, kE4m3>(r)) << 4);
+                from[j] = at < 0 || (kPadded && chunk_of(lane, j) * 16 >= cold.a.D * kItem)
+                              ? cold.zeros
+                              : g.base + at * kItem + (chunk_of(lane, j) << 4);
             }
         }
         slots.pick(number, [&](char *slot) {
@@ -536,8 +558,9 @@ struct Tiles {
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const float v = load1<kE4m3>(
-                        cold.c.v, at + t.head_off + d * 32 + 8 * (r / 4) + 4 * h + (r & 3));
+                    const int e = d * 32 + 8 * (r / 4) + 4 * h + (r & 3);
+                    if (kPadded && e >= cold.D) continue;
+                    const float v = load1<kE4m3>(cold.c.v, at + t.head_off + e);
                     st.o[d][r] += see && !(fabsf(v) < INFINITY) ? v : 0.f;
                     __builtin_amdgcn_sched_barrier(0);  // one at a time: registers, not speed
                 }
@@ -799,9 +822,9 @@ struct Tiles {
     }
 };
 
-template <int D, bool kE4m3, bool kWide>
+template <int D, bool kE4m3, bool kWide, bool kPadded>
 __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileParams tp) {
-    using T = Tiles<D, kE4m3, kWide>;
+    using T = Tiles<D, kE4m3, kWide, kPadded>;
     using Unit = typename T::Unit;
     constexpr int kBlockRows = T::kBlockRows, kSlots = T::kSlots, kWaveLoads = T::kWaveLoads;
     constexpr int kTileThreads = T::kThreads, kTileWaves = T::kWaves;
@@ -1053,7 +1076,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             x[ks] = u32x4{0u, 0u, 0u, 0u};
-            if (valid && t.active) x[ks] = *reinterpret_cast<const u32x4 *>(src + ks * 16);
+            const bool here = !kPadded || ks * 16 + (lane >> 5) * 8 < p.D;
+            if (valid && t.active && here) x[ks] = *reinterpret_cast<const u32x4 *>(src + ks * 16);
         }
         const int k0 = next.tile * T::kKeys, k1 = (next.tile + n) * T::kKeys;
         t.hole = T::holes(p.c, t.table, k0 > t.lo ? k0 : t.lo, k1 < t.hi ? k1 : t.hi, tp.together);
@@ -1105,7 +1129,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         if (n == next.k.tiles) {
             if (kg == 0 && t.active && valid) {
                 const float norm = st.l > 0.f ? p.c.v_scale / st.l : 0.f;
-                uint16_t *o = p.out + (row * p.Hq + hq) * D + (lane >> 5) * 4;
+                uint16_t *o = p.out + (row * p.Hq + hq) * (kPadded ? p.D : D) + (lane >> 5) * 4;
 #pragma unroll
                 for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -1114,7 +1138,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                             (uint64_t)pack_bf16(st.o[d][r] * norm, st.o[d][r + 1] * norm) |
                             ((uint64_t)pack_bf16(st.o[d][r + 2] * norm, st.o[d][r + 3] * norm)
                              << 32);
-                        *reinterpret_cast<uint64_t *>(o + d * 32 + 2 * r) = y;
+                        if (!kPadded || d * 32 + 2 * r < p.D)
+                            *reinterpret_cast<uint64_t *>(o + d * 32 + 2 * r) = y;
                     }
             }
             return;
@@ -1199,9 +1224,10 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 const float norm = l > 0.f ? p.c.v_scale / l : 0.f;
                 const int d = pair / 8 * 32 + pair % 8 / 2 * 8 + (k & 1) * 4 + pair % 2 * 2;
                 const int mm = m0 + r0 + x, jj = mm / G, hh = next.head * G + (mm - jj * G);
-                *reinterpret_cast<uint32_t *>(
-                    p.out + ((int64_t)(next.q.start + jj) * p.Hq + hh) * D + d) =
-                    pack_bf16(v[0] * norm, v[1] * norm);
+                if (!kPadded || d < p.D)
+                    *reinterpret_cast<uint32_t *>(
+                        p.out + ((int64_t)(next.q.start + jj) * p.Hq + hh) * (kPadded ? p.D : D) +
+                        d) = pack_bf16(v[0] * norm, v[1] * norm);
             };
             auto sums = [&](auto pairs_at_once, auto parts_at_once) {
                 constexpr int kPairs = decltype(pairs_at_once)::value;
@@ -1283,12 +1309,20 @@ static int tile_slot_rows(int max_rows, int Hq, int Hkv) {
 }
 static size_t tile_arrival_bytes() { return ((size_t)tile_wgs(false) * 4 + 255) & ~(size_t)255; }
 
+// The head size of the tiles for heads of D, 0 where they do not serve it: a row is
+// loaded 16 bytes at a time.
+static int tile_head(int D, bool e4m3) {
+    if (D > 128 || (e4m3 && D % 16 != 0)) return 0;
+    return D > 64 ? 128 : 64;
+}
+
 size_t attention_ws_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
     (void)B;
-    if (D != 64 && D != 128) return 256;
+    const int head = tile_head(D, false);  // the same for either type of cache
+    if (head == 0) return 256;
     const size_t n = kZeroBytes + tile_arrival_bytes() +
                      (size_t)2 * tile_wgs(tile_wide(max_rows, Hq, Hkv)) *
-                         (size_t)slot_floats(tile_slot_rows(max_rows, Hq, Hkv), D) * 4;
+                         (size_t)slot_floats(tile_slot_rows(max_rows, Hq, Hkv), head) * 4;
     return (n + 255) & ~(size_t)255;
 }
 
@@ -1311,21 +1345,35 @@ static hipError_t launch_tiles(const AttendParams &p, void *ws, hipStream_t s) {
         tp.a.cu = p.cu + b;
         tp.a.ctx = p.ctx + b;
         tp.a.c.table = p.c.table + (int64_t)b * p.c.table_width;
-        if (tile_wide(p.max_rows, p.Hq, p.Hkv))
-            hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3, true>), dim3(tile_wgs(true)),
-                               dim3(Tiles<D, kE4m3, true>::kThreads), 0, s, tp);
-        else
-            hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3, false>), dim3(tile_wgs(false)),
-                               dim3(Tiles<D, kE4m3, false>::kThreads), 0, s, tp);
+        auto go = [&](auto wide, auto padded) {
+            constexpr bool kWide = decltype(wide)::value, kPadded = decltype(padded)::value;
+            hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3, kWide, kPadded>),
+                               dim3(tile_wgs(kWide)),
+                               dim3(Tiles<D, kE4m3, kWide, kPadded>::kThreads), 0, s, tp);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        if (tile_wide(p.max_rows, p.Hq, p.Hkv)) {
+            if (p.D == D) go(yes, no);
+            else go(yes, yes);
+        } else {
+            if (p.D == D) go(no, no);
+            else go(no, yes);
+        }
     }
     return hipGetLastError();
 }
 
 hipError_t launch_attention(const AttendParams &p, bool e4m3, void *ws, hipStream_t s) {
-    if (p.D == 128)
+    // an 8-bit cache may be aligned to 8 bytes only
+    const bool aligned = (((uintptr_t)p.c.k | (uintptr_t)p.c.v) % 16 == 0) &&
+                         (!e4m3 || (p.c.page_stride | p.c.head_stride | p.c.slot_stride) % 16 == 0);
+    switch (aligned ? tile_head(p.D, e4m3) : 0) {
+    case 128:
         return e4m3 ? launch_tiles<128, true>(p, ws, s) : launch_tiles<128, false>(p, ws, s);
-    if (p.D == 64)
+    case 64:
         return e4m3 ? launch_tiles<64, true>(p, ws, s) : launch_tiles<64, false>(p, ws, s);
+    }
     const dim3 grid((unsigned)p.rows, (unsigned)p.Hq);
     if (e4m3) hipLaunchKernelGGL((attend_row_kernel<true>), grid, dim3(kRowThreads), 0, s, p);
     else hipLaunchKernelGGL((attend_row_kernel<false>), grid, dim3(kRowThreads), 0, s, p);

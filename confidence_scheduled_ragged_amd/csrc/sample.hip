@@ -13,6 +13,12 @@
 // are taken in 64 bits once per value. The border of a cut then moves by 1e-15
 // of the sum where a sum of fp32 weights moves it by 1e-6, which at 1e5 entries
 // would change the drawn token of several rows in a hundred.
+//
+// One workgroup counts a row in LDS and finds the drawn value there, then its index
+// in the row. 2003 rows of 151936 (609 MB) take 160 us: reading them once and a half
+// at 5.7 TB/s bounds that, with the LDS atomics (63 us) and vector instructions beside
+// it. Two rows take 27 us: a CU's 1.5e5 atomics (8 us) and a chain of round trips. Rows
+// that need the wide places take eight times as long (1259 us for all 2003).
 #include "argmax_dev.hpp"
 #include "forward.hpp"
 

@@ -233,7 +233,7 @@ def test_graph_replays_with_new_lengths():
 
 
 @pytest.mark.parametrize("rows,ctx", [([4], [61]), ([17, 1, 9], [300, 63, 5]), ([70, 33], [0, 40])])
-@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("D", [64, 128, 96, 136])
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_infinities_that_only_later_rows_see(rows, ctx, D, cache):
     """Values (and keys) that are not finite at a position change no row before
@@ -259,7 +259,7 @@ def test_infinities_that_only_later_rows_see(rows, ctx, D, cache):
                 assert not bool(got[r0 + n - 2:r0 + n, :, 3::7].isfinite().any())
 
 
-@pytest.mark.parametrize("D", [64, 128, 96])
+@pytest.mark.parametrize("D", [64, 128, 96, 136])
 def test_infinities_that_a_window_has_left_behind(D):
     c = make([17, 80], [100, 0], 4, 2, D, 16, seed=13)
     kw = dict(window=20)
@@ -343,3 +343,26 @@ def test_a_smaller_call_after_a_larger_one_and_back():
     for _ in range(3):
         check(small)
         check(big)
+
+
+@pytest.mark.parametrize("D", [8, 16, 24, 40, 48, 72, 80, 104, 112, 120, 136, 192])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_other_head_sizes(D, cache):
+    check(make([3, 1, 40, 17], [40, 300, 0, 129], 4, 2, D, 16, cache, seed=D), **SCALES[cache])
+    check(make([70, 1], [90, 5], 4, 1, D, 7, cache, seed=D, layout="page_slot"), **SCALES[cache])
+
+
+@pytest.mark.parametrize("D", [64, 72, 128])
+def test_an_8_bit_pool_aligned_to_8_bytes(D):
+    c = make([3, 1], [40, 100], 4, 2, D, 16, "e4m3", seed=21)
+    out = torch.zeros((c["cap"], 4, D), dtype=torch.bfloat16)
+    want, tol = ref.attend(c["q"], c["kc"], c["vc"], c["cu"], c["ctx"], c["table"], c["max_rows"],
+                           out=out, **SCALES["e4m3"])
+    pools_ = []
+    for x in (c["kc"], c["vc"]):
+        flat = torch.zeros(x.numel() + 8, dtype=torch.uint8, device=DEV)
+        flat[8:] = x.view(torch.uint8).reshape(-1).to(DEV)
+        pools_.append(flat[8:].view(x.shape).view(x.dtype))
+    got = call(c, *pools_, out.to(DEV), **SCALES["e4m3"])
+    torch.cuda.synchronize()
+    assert bool(((got.cpu().double() - want).abs() <= tol).all())
