@@ -599,21 +599,22 @@ struct Tiles {
     static constexpr int kReads = kE4m3 ? 1 : 2;
     static constexpr int kValueReads = kReads * (D / 32);  // of 16 keys
     struct ValueAddresses {
-        uint32_t at[kValueReads];
+        uint32_t at[kValueReads];  // the second read of 16 bits is kSecond bytes further
     };
+    static constexpr int kSecond = 8 * kRow;
     __device__ static __forceinline__ ValueAddresses value_addresses(uint32_t base, int lane) {
         const int i16 = lane & 15, grp = (lane >> 4) & 1, h = lane >> 5;
+        const int r = kE4m3 ? 8 * (i16 >> 3) + 4 * h + ((i16 >> 1) & 3) : 4 * h + (i16 >> 2);
+        const int c = kE4m3 ? grp : 2 * grp + ((i16 & 3) >> 1);
+        // d and e turn bits of the chunk, which the swizzle leaves to them
+        const uint32_t first =
+            base + (uint32_t)(r * kRow + ((c ^ swizzle<D, kE4m3>(r)) << 4) + (i16 & 1) * 8);
         ValueAddresses v;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-            for (int e = 0; e < kReads; ++e) {
-                const int r = kE4m3 ? 8 * (i16 >> 3) + 4 * h + ((i16 >> 1) & 3)
-                                    : 8 * e + 4 * h + (i16 >> 2);
-                const int c = kE4m3 ? 2 * d + grp : 4 * d + 2 * grp + ((i16 & 3) >> 1);
-                v.at[d * kReads + e] = base + (uint32_t)(r * kRow + ((c ^ swizzle<D, kE4m3>(r)) << 4) +
-                                                         (i16 & 1) * 8);
-            }
+            for (int e = 0; e < kReads; ++e)
+                v.at[d * kReads + e] = first ^ (uint32_t)(kE4m3 ? d << 5 : d << 6 | e << 5);
         return v;
     }
     // The reads are issued and waited for in one piece: as builtins they would wait
@@ -638,26 +639,28 @@ struct Tiles {
                          : "v"(v.at[0]), "v"(v.at[1]), "v"(v.at[2]), "v"(v.at[3]), "i"(kOffset));
         } else if constexpr (D == 64) {
             asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%c8\n\t"
-                         "ds_read_b64_tr_b16 %1, %5 offset:%c8\n\t"
+                         "ds_read_b64_tr_b16 %1, %5 offset:%c9\n\t"
                          "ds_read_b64_tr_b16 %2, %6 offset:%c8\n\t"
-                         "ds_read_b64_tr_b16 %3, %7 offset:%c8\n\t"
+                         "ds_read_b64_tr_b16 %3, %7 offset:%c9\n\t"
                          "s_waitcnt lgkmcnt(0)"
                          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
-                         : "v"(v.at[0]), "v"(v.at[1]), "v"(v.at[2]), "v"(v.at[3]), "i"(kOffset));
+                         : "v"(v.at[0]), "v"(v.at[1]), "v"(v.at[2]), "v"(v.at[3]), "i"(kOffset),
+                           "i"(kOffset + kSecond));
         } else {
             asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%c16\n\t"
-                         "ds_read_b64_tr_b16 %1, %9 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %1, %9 offset:%c17\n\t"
                          "ds_read_b64_tr_b16 %2, %10 offset:%c16\n\t"
-                         "ds_read_b64_tr_b16 %3, %11 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %3, %11 offset:%c17\n\t"
                          "ds_read_b64_tr_b16 %4, %12 offset:%c16\n\t"
-                         "ds_read_b64_tr_b16 %5, %13 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %5, %13 offset:%c17\n\t"
                          "ds_read_b64_tr_b16 %6, %14 offset:%c16\n\t"
-                         "ds_read_b64_tr_b16 %7, %15 offset:%c16\n\t"
+                         "ds_read_b64_tr_b16 %7, %15 offset:%c17\n\t"
                          "s_waitcnt lgkmcnt(0)"
                          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]),
                            "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
                          : "v"(v.at[0]), "v"(v.at[1]), "v"(v.at[2]), "v"(v.at[3]), "v"(v.at[4]),
-                           "v"(v.at[5]), "v"(v.at[6]), "v"(v.at[7]), "i"(kOffset));
+                           "v"(v.at[5]), "v"(v.at[6]), "v"(v.at[7]), "i"(kOffset),
+                           "i"(kOffset + kSecond));
         }
     }
     __device__ static __forceinline__ bf16x8 value_of(const i32x2 (&x)[kValueReads], int d) {
@@ -678,8 +681,8 @@ struct Tiles {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(v.at[2 * d + e] +
-                                                                           16 * kk * kRow));
+                    (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(
+                        v.at[2 * d + e] + 16 * kk * kRow + e * kSecond));
             return __builtin_bit_cast(bf16x8,
                                       __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
         }

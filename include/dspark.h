@@ -425,7 +425,8 @@ dspark_status dspark_append_kv(const dspark_bf16 *q, const dspark_bf16 *k, const
  * (from 0 when window is 0) that the table names:
  *   out[r, h] = sum_s p_s V_s / sum_s p_s,  p_s = exp(scale * (q[r,h] . K_s) - max)
  * with K and V of head h / (Hq / Hkv), statistics in fp32 and one rounding of
- * the result to bf16. A row that sees no position gives zeros.
+ * the result to bf16. A row that sees no position gives zeros, and a position that
+ * a row does not see has no effect on it, whatever the cache holds there.
  * q [rows, Hq, D] bf16, q_row and q_head elements between rows and heads;
  * max_rows bounds the rows of a request (rows past it are untouched); out
  * [rows, Hq, D] bf16, not overlapping q or the cache. D is a multiple of 8 up
