@@ -142,7 +142,7 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
 // with more (prompts) are bound by the matrix and vector instructions of the
 // softmax, which two waves of a SIMD overlap poorly: one workgroup of eight waves a
 // CU, four tiles in LDS, so that keys are read from L2 once for 256 rows. The chunk
-// takes 592 us, 851 TFLOP/s; four prompts of 1882 to 2902 tokens 312 us, 671 TFLOP/s.
+// takes 583 us, 865 TFLOP/s; four prompts of 1882 to 2902 tokens 312 us, 671 TFLOP/s.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds 16 of a query's 32
 // scores of one MFMA (the other 16 sit in lane ^ 32), so the softmax needs one
@@ -225,7 +225,8 @@ __device__ __forceinline__ Request load_request(const AttendParams &p, int b) {
 }
 template <int kBlockRows>
 __device__ __forceinline__ Request scalar_request(const AttendParams &p, int b) {
-    return request_of<kBlockRows>(p, scalar_load(p.cu, b), scalar_load(p.cu, b + 1), scalar_load(p.ctx, b));
+    return request_of<kBlockRows>(p, scalar_load(p.cu, b), scalar_load(p.cu, b + 1),
+                                  scalar_load(p.ctx, b));
 }
 // Positions [lo, hi) that block i of a request needs, its first and last row's
 // positions, and its tiles (one at least: a block that sees nothing still writes
@@ -847,13 +848,15 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     if ((int64_t)p.max_rows * G <= kBlockRows) {
         for (int b = tid; b < p.B; b += kTileThreads) {
             const Request q = load_request<kBlockRows>(p, b);
-            s.before[b + 1] = q.M > 0 ? (uint64_t)(kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, 0).tiles) * p.Hkv : 0;
+            const int tiles = block_of<kBlockRows, T::kKeys>(p, q, 0).tiles;
+            s.before[b + 1] = q.M > 0 ? (uint64_t)(kUnitTiles + tiles) * p.Hkv : 0;
         }
     } else {
         for (int b = wave; b < p.B; b += kTileWaves) {
             const Request q = load_request<kBlockRows>(p, b);
             uint64_t n = 0;
-            for (int i = lane; i < q.blocks; i += kWave) n += kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, i).tiles;
+            for (int i = lane; i < q.blocks; i += kWave)
+                n += kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, i).tiles;
             n = wave_incl_sum_u64(n);
             if (lane == kWave - 1) s.before[b + 1] = n * p.Hkv;
         }
