@@ -140,7 +140,7 @@ def dspark_workspace_init(ws: torch.Tensor) -> None:
         lib().dspark_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)))
 
 
-_WS: Dict[tuple, torch.Tensor] = {}
+_WS: Dict[tuple, list] = {}
 
 
 def _ws_key(device) -> tuple:
@@ -151,18 +151,18 @@ def _ws_key(device) -> tuple:
 
 def workspace(B: int, gamma: int, V: int, device) -> torch.Tensor:
     """A zero-initialised workspace of the required size, cached per device.
-    Calls sharing it must not overlap in time (one stream, or ordered)."""
+    Calls sharing it must not overlap in time (one stream, or ordered).
+    One that has become too small stays allocated: a captured graph may use it."""
     device = torch.device(device)
     need = dspark_workspace_bytes(B, gamma, V)
     if need == 0:
         raise ValueError(f"invalid sizes B={B} gamma={gamma} V={V}")
-    key = _ws_key(device)
-    ws = _WS.get(key)
-    if ws is None or ws.numel() < need:
+    held = _WS.setdefault(_ws_key(device), [])
+    if not held or held[-1].numel() < need:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         dspark_workspace_init(ws)
-        _WS[key] = ws
-    return ws
+        held.append(ws)
+    return held[-1]
 
 
 # ------------------------------------------------------------- entry points
@@ -520,11 +520,12 @@ def dspark_step_noalloc(hidden, w, bias, temps, tokens, logits, mode, cutoff=Non
 def dspark_step_status(ws=None, status=None, device=None):
     """The fused step's give-up flag of a workspace, read and cleared on the
     device: an int32 [1] tensor, 0 when no call since the last read gave up its
-    bounded wait. ws defaults to the binding's cached workspace of `device`."""
+    bounded wait. ws defaults to the binding's newest workspace of `device`."""
     if ws is None:
-        ws = _WS.get(_ws_key(device if device is not None else "cuda"))
-        if ws is None:
+        held = _WS.get(_ws_key(device if device is not None else "cuda"))
+        if not held:
             raise ValueError("no workspace has been used on this device")
+        ws = held[-1]
     _need(ws, "ws", torch.uint8)
     status = torch.empty(1, dtype=torch.int32, device=ws.device) if status is None else status
     _need(status, "status", torch.int32, (1,))
