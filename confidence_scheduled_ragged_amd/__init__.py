@@ -140,29 +140,72 @@ def dspark_workspace_init(ws: torch.Tensor) -> None:
         lib().dspark_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)))
 
 
-_WS: Dict[tuple, list] = {}
+class _Kept:
+    """The workspaces of one device that calls without one of their own use."""
+
+    def __init__(self):
+        self.held = []         # zeroed outside of captures, by size
+        self.capture = 0       # the last capture that had to make one, and that one
+        self.captured = None
+        self.used = None       # by the last call
+
+
+_WS: Dict[tuple, _Kept] = {}
 
 
 def _ws_key(device) -> tuple:
-    device = torch.device(device)
+    device = device if isinstance(device, torch.device) else torch.device(device)
     idx = device.index if device.index is not None else torch.cuda.current_device()
     return (device.type, idx)
 
 
+def _capture_id(device) -> int:
+    """The capture that the current stream of `device` is in, 0 if in none."""
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            return 0
+    status, capture = ctypes.c_int(), ctypes.c_ulonglong()
+    error = lib().hipStreamGetCaptureInfo(_stream(device), ctypes.byref(status),
+                                          ctypes.byref(capture))
+    if error:
+        raise RuntimeError(f"hipStreamGetCaptureInfo: error {error}")
+    return capture.value
+
+
+def _kept_workspace(cache: Dict[tuple, _Kept], need: int, device) -> torch.Tensor:
+    """A zero-filled workspace of at least `need` bytes. One that has become too
+    small stays allocated: a captured graph may use it. One that a capture has to
+    make is zeroed by the graph only, so it serves that capture alone."""
+    key = _ws_key(device)
+    kept = cache.get(key)
+    if kept is None:
+        kept = cache[key] = _Kept()
+    if kept.held and kept.held[-1].numel() >= need:
+        kept.used = kept.held[-1]
+        return kept.used
+    capture = _capture_id(device)
+    if capture and kept.capture == capture and kept.captured.numel() >= need:
+        kept.used = kept.captured
+        return kept.used
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    dspark_workspace_init(ws)
+    if capture:
+        kept.capture, kept.captured = capture, ws
+    else:
+        kept.held.append(ws)
+    kept.used = ws
+    return ws
+
+
 def workspace(B: int, gamma: int, V: int, device) -> torch.Tensor:
-    """A zero-initialised workspace of the required size, cached per device.
-    Calls sharing it must not overlap in time (one stream, or ordered).
-    One that has become too small stays allocated: a captured graph may use it."""
+    """A zero-initialised workspace of the required size, cached per device (a
+    capture for which none is large enough gets its own). Calls sharing it must
+    not overlap in time (one stream, or ordered)."""
     device = torch.device(device)
     need = dspark_workspace_bytes(B, gamma, V)
     if need == 0:
         raise ValueError(f"invalid sizes B={B} gamma={gamma} V={V}")
-    held = _WS.setdefault(_ws_key(device), [])
-    if not held or held[-1].numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        dspark_workspace_init(ws)
-        held.append(ws)
-    return held[-1]
+    return _kept_workspace(_WS, need, device)
 
 
 # ------------------------------------------------------------- entry points
@@ -520,12 +563,13 @@ def dspark_step_noalloc(hidden, w, bias, temps, tokens, logits, mode, cutoff=Non
 def dspark_step_status(ws=None, status=None, device=None):
     """The fused step's give-up flag of a workspace, read and cleared on the
     device: an int32 [1] tensor, 0 when no call since the last read gave up its
-    bounded wait. ws defaults to the binding's newest workspace of `device`."""
+    bounded wait. ws defaults to the binding's workspace of `device` that the last
+    call without one of its own used."""
     if ws is None:
-        held = _WS.get(_ws_key(device if device is not None else "cuda"))
-        if not held:
+        kept = _WS.get(_ws_key(device if device is not None else "cuda"))
+        if kept is None or kept.used is None:
             raise ValueError("no workspace has been used on this device")
-        ws = held[-1]
+        ws = kept.used
     _need(ws, "ws", torch.uint8)
     status = torch.empty(1, dtype=torch.int32, device=ws.device) if status is None else status
     _need(status, "status", torch.int32, (1,))
@@ -613,24 +657,17 @@ def dspark_attention_workspace_bytes(B: int, max_rows: int, Hq: int, Hkv: int, D
     return int(lib().dspark_attention_workspace_bytes(B, max_rows, Hq, Hkv, D))
 
 
-_ATTN_WS: Dict[int, list] = {}
+_ATTN_WS: Dict[tuple, _Kept] = {}
 
 
 def attention_workspace(B: int, max_rows: int, Hq: int, Hkv: int, D: int, device) -> torch.Tensor:
     """A zero-initialised workspace of dspark_verify_attention, cached per
-    device. Calls sharing it must not overlap in time (one stream, or ordered).
-    One that has become too small stays allocated: a captured graph may use it."""
+    device as by workspace(). Calls sharing it must not overlap in time (one
+    stream, or ordered)."""
     need = lib().dspark_attention_workspace_bytes(B, max_rows, Hq, Hkv, D)
     if need == 0:
         raise ValueError(f"invalid sizes B={B} max_rows={max_rows} Hq={Hq} Hkv={Hkv} D={D}")
-    device = device if isinstance(device, torch.device) else torch.device(device)
-    index = device.index if device.index is not None else torch.cuda.current_device()
-    held = _ATTN_WS.setdefault(index, [])
-    if not held or held[-1].numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        dspark_workspace_init(ws)
-        held.append(ws)
-    return held[-1]
+    return _kept_workspace(_ATTN_WS, need, device)
 
 
 def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, max_rows,
