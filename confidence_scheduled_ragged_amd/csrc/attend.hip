@@ -1180,6 +1180,9 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         }
         __syncthreads();
         if (!s.last) return;
+        // A part whose row saw nothing has no maximum and holds zeros. One whose scores
+        // were NaN has none either (fmaxf drops NaN), but a sum and values that are
+        // NaN: no part is left out, whatever its factor.
         // First the factor of every part and row, as many rows at a time as s.join
         // holds, then the pairs of elements: 16 loads are on their way a thread,
         // two parts of eight pairs or, where there are few pairs, 16 parts of one.
@@ -1215,7 +1218,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
 #pragma unroll
             for (int u = 0; u < kTable / T::kThreads; ++u) {
                 const int i = u * T::kThreads + tid;
-                if (i < nr * parts) share[i] = factor[i] != 0.f ? factor[i] * ml[u][1] : 0.f;
+                if (i < nr * parts) share[i] = factor[i] * ml[u][1];
             }
             __syncthreads();
             const int items = nr * (D / 2);
@@ -1266,10 +1269,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                             for (int u = 0; u < kPairs; ++u) {
                                 const float f = factor[(w0 + w) * nr + x[u]];
                                 l[u] += share[(w0 + w) * nr + x[u]];
-                                if (f != 0.f) {
-                                    v[u][0] += f * y[w][u][0];
-                                    v[u][1] += f * y[w][u][1];
-                                }
+                                v[u][0] += f * y[w][u][0];
+                                v[u][1] += f * y[w][u][1];
                             }
                         }
                     }
