@@ -88,10 +88,12 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
         float top = x;
 #pragma unroll
         for (int off = kWave / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+        // fmaxf drops NaN: keys may be there that leave no maximum
+        if (!__any(at >= 0)) continue;
         const float m1 = fmaxf(m, top);
-        if (m1 == -INFINITY) continue;
-        const float keep = expf(m - m1);
-        const float w = at >= 0 ? expf(x - m1) : 0.f;
+        const float base = m1 == -INFINITY ? 0.f : m1;
+        const float keep = expf(m - base);  // 0 before the first maximum
+        const float w = at >= 0 ? expf(x - base) : 0.f;
         m = m1;
         total = total * keep + wave_sum_f32(w);
         p_s[lane] = w;

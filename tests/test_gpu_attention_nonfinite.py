@@ -10,9 +10,9 @@ from test_gpu_attention import DEV, SCALES, call, make, pools
 pytestmark = pytest.mark.gpu
 
 NAN, INF = float("nan"), float("inf")
-# head size, cache, positions of a tile
+# head size, cache, positions of a tile (of a step of the row kernel over 128)
 HEADS = [(64, "bf16", 128), (128, "bf16", 64), (96, "bf16", 64), (64, "e4m3", 256),
-         (128, "e4m3", 128)]
+         (128, "e4m3", 128), (136, "bf16", 64), (192, "e4m3", 64)]
 
 
 def run(c, cache, **kw):
