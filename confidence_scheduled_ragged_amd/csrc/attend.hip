@@ -1329,10 +1329,15 @@ size_t attention_ws_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
     (void)B;
     const int head = tile_head(D, false);  // the same for either type of cache
     if (head == 0) return 256;
-    const size_t n = kZeroBytes + tile_arrival_bytes() +
-                     (size_t)2 * tile_wgs(tile_wide(max_rows, Hq, Hkv)) *
-                         (size_t)slot_floats(tile_slot_rows(max_rows, Hq, Hkv), head) * 4;
-    return (n + 255) & ~(size_t)255;
+    auto need = [&](int rows) {
+        return (size_t)2 * tile_wgs(tile_wide(rows, Hq, Hkv)) *
+               (size_t)slot_floats(tile_slot_rows(rows, Hq, Hkv), head) * 4;
+    };
+    size_t slots = need(max_rows);
+    // A call may have fewer rows, and the kernel for those twice the workgroups.
+    const int narrow = kNarrowRows / (Hq / Hkv);  // the most rows it takes
+    if (tile_wide(max_rows, Hq, Hkv) && narrow > 0 && need(narrow) > slots) slots = need(narrow);
+    return (kZeroBytes + tile_arrival_bytes() + slots + 255) & ~(size_t)255;
 }
 
 template <int D, bool kE4m3>

@@ -447,7 +447,8 @@ dspark_status dspark_verify_attention(const dspark_bf16 *q, long long q_row, lon
                                       float scale, dspark_bf16 *out, void *ws, size_t ws_bytes,
                                       void *stream);
 
-/* Scratch bytes of dspark_verify_attention for these sizes; 0 for invalid ones. */
+/* Scratch bytes of dspark_verify_attention for these sizes, enough for a call of
+ * fewer rows too; 0 for invalid ones. */
 size_t dspark_attention_workspace_bytes(int B, int max_rows, int Hq, int Hkv, int D);
 
 /*

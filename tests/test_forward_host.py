@@ -116,3 +116,20 @@ def test_binding_refuses_cpu_tensors_and_bad_layouts():
         dspark.dspark_verify_attention(bf(3, 4, 64), cache, cache[:3], i32(2), i32(1), i32(1, 4), 1)
     with pytest.raises(ValueError):
         dspark.dspark_sample_accept(bf(6, 10), None, i32(4), i32(3, 2), torch.zeros(6))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(32, 8), (8, 8), (64, 8), (40, 8), (9, 1), (127, 1), (128, 1),
+                                    (129, 1), (300, 1), (6, 2)])
+@pytest.mark.parametrize("D", [64, 72, 128, 136])
+def test_attention_workspace_serves_every_smaller_call(L, Hq, Hkv, D):
+    """A call has fewer rows than the most its workspace was made for."""
+    sizes = [L.dspark_attention_workspace_bytes(1, n, Hq, Hkv, D) for n in range(1, 400)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_attention_accepts_the_workspace_of_its_arguments(L):
+    """rows below max_rows: checked against the header's size, one byte below it refused."""
+    for rows, most in ((32, 40), (1, 64), (5, 5000)):
+        need = L.dspark_attention_workspace_bytes(4, rows, 32, 8, 128)
+        assert need <= L.dspark_attention_workspace_bytes(4, most, 32, 8, 128)
+        assert attend_call(L, rows=rows, max_rows=most, wsb=need - 1) == EWS
