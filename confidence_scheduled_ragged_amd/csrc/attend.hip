@@ -328,13 +328,17 @@ struct Tiles {
     static constexpr int kWaveRows = kKeys / kStagers;   // rows that each of them stages
     static constexpr int kWaveLoads = kHalfSlot / kStagers / 1024;  // of 1 KiB
     static constexpr int kEntries = kWaveRows / 16;      // 16 rows each
+    static constexpr int kRowWords = (kWaveRows + 63) / 64;  // of a bit for each of them
+    static_assert(64 % kLoadRows == 0 && (kRowWords == 1 || kWaveRows % 64 == 0),
+                  "the rows of a load share a word");
 
     struct Lds {
         uint64_t before[kGroupRequests + 1];
         uint64_t part[kWaves];
         float join[16 * (kWaves / 2) * kWave];
         f32x2 ml[kWaves / 2 * kWave];
-        uint64_t bad[kSlots][kStagers];  // rows whose values were not all finite, per staging wave
+        // rows whose values were not all finite, per staging wave
+        uint64_t bad[kSlots][kStagers * kRowWords];
         int last;
     };
 
@@ -520,7 +524,7 @@ struct Tiles {
     __device__ static __forceinline__ void scrub(Lds &s, const Slots &slots, int n, int lane) {
         const int w = wave_id();
         if (w < kStagers) return;
-        uint64_t rows = 0;
+        uint64_t rows[kRowWords] = {};
         typedef __attribute__((address_space(3))) u32x4 *Words;
         const uint32_t slot = slots.address(n);
 #pragma unroll 1
@@ -535,11 +539,18 @@ struct Tiles {
                 for (int i = 0; i < 4; ++i) x[i] = good_part(x[i]);
                 *at = x;
             }
+            uint64_t here = 0;
             for (int r = 0; r < kLoadRows; ++r)
                 if (m >> (r * kChunks) & ((1ull << kChunks) - 1))
-                    rows |= 1ull << (j * kLoadRows + r);
+                    here |= 1ull << (j * kLoadRows % 64 + r);
+#pragma unroll
+            for (int i = 0; i < kRowWords; ++i)
+                if (j * kLoadRows / 64 == i) rows[i] |= here;
         }
-        if (lane == 0) s.bad[n][w - kStagers] = rows;
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < kRowWords; ++i) s.bad[n][(w - kStagers) * kRowWords + i] = rows[i];
+        }
         wait_loads<63>();  // LDS accesses only
     }
     // The values that scrub left out of 32 keys, from the cache again: to the
@@ -552,7 +563,8 @@ struct Tiles {
         const AttendParams cold = params_again().a;
 #pragma unroll 1
         for (int y = sub * 32; y < sub * 32 + 32; ++y) {
-            if (!(bad[y / kWaveRows] >> (y % kWaveRows) & 1)) continue;
+            if (!(bad[y / kWaveRows * kRowWords + y % kWaveRows / 64] >> (y % kWaveRows % 64) & 1))
+                continue;
             const int key = tile * kKeys + y;
             const int64_t at = slot_offset(cold.c, t.table, key, 0);
             if (at < 0) continue;
@@ -1020,7 +1032,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 const uint64_t *bad = s.bad[number];
                 uint64_t any = 0;
 #pragma unroll
-                for (int i = 0; i < T::kStagers; ++i) any |= bad[i];
+                for (int i = 0; i < T::kStagers * T::kRowWords; ++i) any |= bad[i];
                 if (any) {
 #pragma unroll 1
                     for (int i = 0; i < each; ++i)

@@ -88,3 +88,21 @@ def test_values_that_are_nan_in_a_tile_of_their_own(D, cache, keys):
         got = run(c, cache)[0]
         assert bool(got[:, 1::3].isnan().all())
         assert bool(got[:, 0::3].isfinite().all())
+
+
+@pytest.mark.parametrize("D,cache,keys", HEADS)
+@pytest.mark.parametrize("rows", [2, 17])
+def test_every_row_of_a_tile_seen_in_part(D, cache, keys, rows):
+    """A value that is NaN at one position of the last tile, wherever in it: the rows
+    from it on are NaN in its elements, the others are as they were."""
+    for at in list(range(0, keys, 23)) + [keys // 2, keys - 1]:
+        ctx = 2 * keys + at - rows // 2
+        c = make([rows], [ctx], 8, 2, D, 16, cache, seed=34)
+        clean = run(c, cache)
+        poison(c, "vc", 0, [2 * keys + at], NAN, slice(0, None, 5))
+        got = run(c, cache)
+        sees = torch.arange(c["cap"]) >= rows // 2
+        sees[rows:] = False
+        assert bool(got[sees][:, :, ::5].isnan().all()), at
+        got[sees] = torch.where(got[sees].isnan(), clean[sees], got[sees])
+        assert torch.equal(got, clean), at
