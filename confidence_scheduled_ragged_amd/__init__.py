@@ -88,9 +88,9 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> torch.Tensor:
+def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, gpu=None) -> torch.Tensor:
     if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
+            and (shape is None or t.shape == shape) and (gpu is None or t.get_device() == gpu)):
         return t
     # what of it is wrong
     if not isinstance(t, torch.Tensor):
@@ -103,6 +103,8 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> torch.T
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if gpu is not None and t.get_device() != gpu:
+        raise ValueError(f"{name} must be on GPU {gpu} as the call's other tensors (got {t.device})")
     return t
 
 
@@ -583,12 +585,13 @@ _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
 
 def _paged(k_cache, v_cache, cu_seqlens, ctx_lens, block_table):
-    """Checks the paged cache and the packed batch's lengths; returns B, the
-    cache's type, sizes and strides."""
+    """Checks the paged cache and the packed batch's lengths; returns the index of
+    their GPU, B, the cache's type, sizes and strides."""
     shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape, [pages, Hkv, page_size, D]")
-    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.get_device() != k_cache.get_device():
+    gpu = k_cache.get_device()
+    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.get_device() != gpu:
         raise ValueError(f"the caches must be on one GPU (got {k_cache.device}, {v_cache.device})")
     if dtype not in _CACHE_TYPES or v_cache.dtype is not dtype:
         raise TypeError(f"the caches must be bfloat16 or float8_e4m3fn (got {dtype}, "
@@ -596,18 +599,20 @@ def _paged(k_cache, v_cache, cu_seqlens, ctx_lens, block_table):
     if v_cache.stride() != strides or strides[3] != 1:
         raise ValueError("k_cache and v_cache must share strides, with D contiguous")
     B = cu_seqlens.numel() - 1
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    _need(ctx_lens, "ctx_lens", torch.int32, (B,))
-    _need(block_table, "block_table", torch.int32)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, None, gpu)
+    _need(ctx_lens, "ctx_lens", torch.int32, (B,), gpu)
+    _need(block_table, "block_table", torch.int32, None, gpu)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, pages of a request)")
-    return B, _CACHE_TYPES[dtype], shape, strides
+    return gpu, B, _CACHE_TYPES[dtype], shape, strides
 
 
-def _packed_heads(t, name, rows, heads, D):
+def _packed_heads(t, name, rows, heads, D, gpu):
     """Checks packed [rows, heads, D] bf16 with rows at any stride; returns its strides."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} must be on GPU {gpu} as the caches (got {t.device})")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16} (got {t.dtype})")
     if t.shape != (rows, heads, D):
@@ -626,28 +631,28 @@ def dspark_append_kv(q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cac
     heads side by side), cos and sin [positions, rot / 2] fp32, ctx_lens [B]
     tokens cached before the call, block_table [B, width] int32, k_cache and
     v_cache [pages, Hkv, page_size, D] bf16 or float8_e4m3fn."""
-    B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(k_cache, v_cache, cu_seqlens,
-                                                             ctx_lens, block_table)
+    gpu, B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(
+        k_cache, v_cache, cu_seqlens, ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
-    qs = _packed_heads(q, "q", rows, Hq, D)
-    ks = _packed_heads(k, "k", rows, Hkv, D)
-    vs = _packed_heads(v, "v", rows, Hkv, D)
+    qs = _packed_heads(q, "q", rows, Hq, D, gpu)
+    ks = _packed_heads(k, "k", rows, Hkv, D, gpu)
+    vs = _packed_heads(v, "v", rows, Hkv, D, gpu)
     if (qs[1] != D and Hq > 1) or ((ks[1] != D or vs[1] != D) and Hkv > 1):
         raise ValueError("q, k and v must have their heads side by side")
-    _need(cos, "cos", torch.float32)
+    _need(cos, "cos", torch.float32, None, gpu)
     angles = cos.shape
-    _need(sin, "sin", torch.float32, angles)
+    _need(sin, "sin", torch.float32, angles, gpu)
     if len(angles) != 2:
         raise ValueError("cos must have shape (positions, rotated pairs)")
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (rows, Hq, D))
+    _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
     status = lib().dspark_append_kv(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], ks[0], vs[0], cos.data_ptr(),
         sin.data_ptr(), angles[0], angles[1], 1 if interleaved else 0, cu_seqlens.data_ptr(),
         ctx_lens.data_ptr(), B, rows, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), kind,
         pages, page, ps, hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
-        out.data_ptr(), _raw_stream(q.get_device()))
+        out.data_ptr(), _raw_stream(gpu))
     if status:
         _ok("dspark_append_kv", status)
     return out
@@ -678,24 +683,24 @@ def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_tab
     rows of a request (1 for plain decoding, gamma + 1 for a verify window, any
     number for a prompt chunk); window > 0 keeps the last `window` positions;
     scale defaults to D ** -0.5. Returns out [rows, Hq, D] bf16."""
-    B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(k_cache, v_cache, cu_seqlens,
-                                                             ctx_lens, block_table)
+    gpu, B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(
+        k_cache, v_cache, cu_seqlens, ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
-    qs = _packed_heads(q, "q", rows, Hq, D)
+    qs = _packed_heads(q, "q", rows, Hq, D, gpu)
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (rows, Hq, D))
+    _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
     max_rows = min(int(max_rows), rows)
     if ws is None:
         ws = attention_workspace(B, max_rows, Hq, Hkv, D, q.device)
     else:
-        _need(ws, "ws", torch.uint8)
+        _need(ws, "ws", torch.uint8, None, gpu)
     status = lib().dspark_verify_attention(
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), kind, pages, page, ps,
         hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
         cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, rows, max_rows, Hq, Hkv, D, int(window),
         D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(q.get_device()))
+        _raw_stream(gpu))
     if status:
         _ok("dspark_verify_attention", status)
     return out
@@ -714,16 +719,17 @@ def dspark_sample_accept(logits, packed_src_row, cu_seqlens, tokens, uniforms, t
     V = logits.shape[-1]
     if logits.numel() != cap * V:
         raise ValueError("logits must hold B*(gamma+1) rows of V entries")
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    _need(tokens, "tokens", torch.int32)
-    _need(uniforms, "uniforms", torch.float32, (cap,))
+    gpu = logits.get_device()
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), gpu)
+    _need(tokens, "tokens", torch.int32, None, gpu)
+    _need(uniforms, "uniforms", torch.float32, (cap,), gpu)
     if packed_src_row is not None:
-        _need(packed_src_row, "packed_src_row", torch.int32, (cap,))
+        _need(packed_src_row, "packed_src_row", torch.int32, (cap,), gpu)
     for t, n in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")):
         if t is not None:
-            _need(t, n, torch.float32, (B,))
+            _need(t, n, torch.float32, (B,), gpu)
     if top_k is not None:
-        _need(top_k, "top_k", torch.int32, (B,))
+        _need(top_k, "top_k", torch.int32, (B,), gpu)
     dev = tokens.device
     out = out or {}
     smp = out.get("packed_sample")
@@ -732,16 +738,16 @@ def dspark_sample_accept(logits, packed_src_row, cu_seqlens, tokens, uniforms, t
     smp = torch.full((cap,), -1, dtype=torch.int32, device=dev) if smp is None else smp
     acc = torch.empty(B, dtype=torch.int32, device=dev) if acc is None else acc
     bon = torch.empty(B, dtype=torch.int32, device=dev) if bon is None else bon
-    _need(smp, "packed_sample", torch.int32, (cap,))
-    _need(acc, "accepted", torch.int32, (B,))
-    _need(bon, "bonus", torch.int32, (B,))
-    ws = workspace(B, g1 - 1, V, dev) if ws is None else _need(ws, "ws", torch.uint8)
+    _need(smp, "packed_sample", torch.int32, (cap,), gpu)
+    _need(acc, "accepted", torch.int32, (B,), gpu)
+    _need(bon, "bonus", torch.int32, (B,), gpu)
+    ws = workspace(B, g1 - 1, V, dev) if ws is None else _need(ws, "ws", torch.uint8, None, gpu)
     at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     status = lib().dspark_sample_accept(
         logits.data_ptr(), at(packed_src_row), cu_seqlens.data_ptr(), tokens.data_ptr(),
         uniforms.data_ptr(), at(temperature), at(top_k), at(top_p), at(min_p), B, g1 - 1, V,
         smp.data_ptr(), acc.data_ptr(), bon.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(tokens.get_device()))
+        _raw_stream(gpu))
     if status:
         _ok("dspark_sample_accept", status)
     return smp, acc, bon

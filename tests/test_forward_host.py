@@ -133,3 +133,59 @@ def test_attention_accepts_the_workspace_of_its_arguments(L):
         need = L.dspark_attention_workspace_bytes(4, rows, 32, 8, 128)
         assert need <= L.dspark_attention_workspace_bytes(4, most, 32, 8, 128)
         assert attend_call(L, rows=rows, max_rows=most, wsb=need - 1) == EWS
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it is on a GPU, for checks that come before any call."""
+    gpu = 0
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", self.gpu))
+
+    def get_device(self):
+        return self.gpu
+
+
+def on_gpu(x, gpu=0):
+    x = x.as_subclass(OnGpu)
+    x.gpu = gpu
+    return x
+
+
+def forward_args():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    f32 = torch.zeros
+    cache = dict(cu_seqlens=i32(2), ctx_lens=i32(1), block_table=i32(1, 4),
+                 k_cache=bf(4, 2, 16, 64), v_cache=bf(4, 2, 16, 64))
+    append = dict(q=bf(3, 4, 64), k=bf(3, 2, 64), v=bf(3, 2, 64), cos=f32(9, 32), sin=f32(9, 32),
+                  out=bf(3, 4, 64), **cache)
+    attend = dict(q=bf(3, 4, 64), max_rows=3, out=bf(3, 4, 64),
+                  ws=torch.zeros(1 << 20, dtype=torch.uint8), **cache)
+    sample = dict(logits=bf(6, 10), packed_src_row=i32(6), cu_seqlens=i32(4), tokens=i32(3, 2),
+                  uniforms=f32(6), temperature=f32(3), top_k=i32(3), top_p=f32(3), min_p=f32(3),
+                  packed_sample=i32(6), accepted=i32(3), bonus=i32(3),
+                  ws=torch.zeros(1 << 20, dtype=torch.uint8))
+    return [(dspark.dspark_append_kv, append), (dspark.dspark_verify_attention, attend),
+            (dspark.dspark_sample_accept, sample)]
+
+
+@pytest.mark.parametrize("i,moved", [(i, k) for i, (_, a) in enumerate(forward_args())
+                                     for k, v in a.items() if isinstance(v, torch.Tensor)])
+def test_binding_refuses_tensors_on_different_gpus(monkeypatch, i, moved):
+    """One tensor on another GPU than all others, whichever it is."""
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 0  # no call reaches a device
+    monkeypatch.setattr(dspark, "lib", Lib)
+    monkeypatch.setattr(dspark, "_raw_stream", lambda index: 0)
+    fn, args = forward_args()[i]
+
+    def call(other):
+        a = {k: on_gpu(v, 1 if k == other else 0) if isinstance(v, torch.Tensor) else v
+             for k, v in args.items()}
+        if fn is dspark.dspark_sample_accept:
+            a["out"] = {k: a.pop(k) for k in ("packed_sample", "accepted", "bonus")}
+        return fn(**a)
+    call(None)
+    with pytest.raises(ValueError, match="GPU"):
+        call(moved)
