@@ -16,6 +16,14 @@ namespace dspark {
 constexpr int kMaxHeadDim = 256;
 constexpr int kRowThreads = 64;
 
+// Contexts are taken as at most this many positions, so that those of the call's
+// rows (2^24 at most) and of a tile past them fit in 32 bits.
+constexpr int kMaxContext = 0x7FFFFFFF - (1 << 25) + 1;
+static_assert(DSPARK_MAX_ROWS <= 1 << 24, "positions of the rows");
+__device__ __forceinline__ int context_of(int ctx) {
+    return ctx < 0 ? 0 : (ctx > kMaxContext ? kMaxContext : ctx);
+}
+
 template <bool kE4m3>
 __device__ __forceinline__ void load8(const void *pool, int64_t at, float *x) {
     if (kE4m3) {
@@ -63,7 +71,7 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
     const int kvh = h / (p.Hq / p.Hkv);
     // positions past the table's width have no page
     const int64_t width = (int64_t)p.c.table_width * p.c.page;
-    const int64_t pos = (int64_t)(p.ctx[b] < 0 ? 0 : p.ctx[b]) + j;
+    const int64_t pos = (int64_t)context_of(p.ctx[b]) + j;
     const int64_t end = pos + 1 < width ? pos + 1 : width;
     const int64_t begin = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
     const int32_t *row = p.c.table + (int64_t)b * p.c.table_width;
@@ -216,7 +224,7 @@ __device__ __forceinline__ Request request_of(const AttendParams &p, int s, int 
     e = e < s ? s : (e > p.rows ? p.rows : e);
     const int n = e - s < p.max_rows ? e - s : p.max_rows;
     q.start = s;
-    q.ctx = c < 0 ? 0 : (c > (1 << 30) ? 1 << 30 : c);
+    q.ctx = context_of(c);
     q.M = n * (p.Hq / p.Hkv);
     q.blocks = (q.M + kBlockRows - 1) / kBlockRows;
     return q;

@@ -428,7 +428,8 @@ dspark_status dspark_append_kv(const dspark_bf16 *q, const dspark_bf16 *k, const
  * the result to bf16. A row that sees no position gives zeros, and a position that
  * a row does not see has no effect on it, whatever the cache holds there.
  * q [rows, Hq, D] bf16, q_row and q_head elements between rows and heads;
- * max_rows bounds the rows of a request (rows past it are untouched); out
+ * max_rows bounds the rows of a request (rows past it are untouched); contexts
+ * above 2^31 - 2^25 count as that many, negative ones as none; out
  * [rows, Hq, D] bf16, not overlapping q or the cache. D is a multiple of 8 up
  * to 256. q, out, and the caches with all their strides are aligned to 16
  * bytes (e4m3 caches to 8), else DSPARK_ERR_ALIGN. ws: at least
