@@ -135,8 +135,12 @@ def main():
     ap.add_argument("--cache", choices=("bf16", "e4m3"), default="bf16")
     ap.add_argument("--graph", action="store_true", help="capture a step and replay it")
     a = ap.parse_args()
-    target = Target(cache=BF16 if a.cache == "bf16" else torch.float8_e4m3fn)
-    loop = Loop(target, [[5, 17, 300], list(range(40, 90)), [7] * 20, [999]])
+    prompts, gamma, page = [[5, 17, 300], list(range(40, 90)), [7] * 20, [999]], 4, 16
+    # rows past the angles' tables or the requests' pages would be left out
+    longest = max(len(p) for p in prompts) + a.steps * (gamma + 1)
+    target = Target(cache=BF16 if a.cache == "bf16" else torch.float8_e4m3fn, page=page,
+                    pages=max(512, len(prompts) * -(-longest // page)), longest=max(1024, longest))
+    loop = Loop(target, prompts, gamma)
     out = [[t] for t in loop.root.tolist()]
     run = loop.step
     if a.graph:
