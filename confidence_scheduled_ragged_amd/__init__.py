@@ -682,7 +682,9 @@ def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_tab
     position ctx_lens[b] + j, which the cache already holds. max_rows bounds the
     rows of a request (1 for plain decoding, gamma + 1 for a verify window, any
     number for a prompt chunk); window > 0 keeps the last `window` positions;
-    scale defaults to D ** -0.5. Returns out [rows, Hq, D] bf16."""
+    scale defaults to D ** -0.5. Returns out [rows, Hq, D] bf16. Without ws the
+    call uses attention_workspace(), one for all streams of the GPU: calls on
+    several streams at a time need one each."""
     gpu, B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(
         k_cache, v_cache, cu_seqlens, ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
@@ -712,7 +714,8 @@ def dspark_sample_accept(logits, packed_src_row, cu_seqlens, tokens, uniforms, t
     bonus). uniforms fp32 [B*(gamma+1)] in [0, 1), one per packed row;
     temperature (<= 0: greedy), top_p, min_p fp32 [B] and top_k int32 [B] (0:
     off) per request, None for temperature 1 and no filter. packed_src_row None
-    means `logits` is already packed."""
+    means `logits` is already packed. Without ws the call uses workspace(), one for
+    all streams of the GPU: calls on several streams at a time need one each."""
     B, g1 = tokens.shape
     cap = B * g1
     _need(logits, "logits", torch.bfloat16)

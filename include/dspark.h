@@ -424,9 +424,17 @@ dspark_status dspark_append_kv(const dspark_bf16 *q, const dspark_bf16 *k, const
  * the request. A row at position t sees positions max(0, t - window + 1) .. t
  * (from 0 when window is 0) that the table names:
  *   out[r, h] = sum_s p_s V_s / sum_s p_s,  p_s = exp(scale * (q[r,h] . K_s) - max)
- * with K and V of head h / (Hq / Hkv), statistics in fp32 and one rounding of
- * the result to bf16. A row that sees no position gives zeros, and a position that
- * a row does not see has no effect on it, whatever the cache holds there.
+ * with K and V of head h / (Hq / Hkv), scores, statistics and both sums in fp32,
+ * and the result rounded once to bf16. Heads up to 128 also round each p_s to bf16
+ * for its product with V_s (not for the sum of p_s), as the matrix instructions
+ * take it: half a step, 2^-8 of each weight, so that the result is off by at most
+ * 2^-8 of the weighted mean of |V| beside its own rounding (measured: 2.1e-3 to
+ * 2.3e-3 of the result in the mean square, 1.7e-3 without). Larger heads, and 8-bit
+ * caches or head sizes that 16-byte loads do not fit, keep fp32 there.
+ * A row that sees no position gives zeros, and a position that a row does not see
+ * has no effect on it, whatever the cache holds there. NaN and infinities that a
+ * row does see, or NaN in its query, reach its result; a score of -inf weighs
+ * nothing, and a row of nothing else gives zeros.
  * q [rows, Hq, D] bf16, q_row and q_head elements between rows and heads;
  * max_rows bounds the rows of a request (rows past it are untouched); contexts
  * above 2^31 - 2^25 count as that many, negative ones as none; out

@@ -5,6 +5,7 @@ import torch
 
 import __graft_entry__  # noqa: F401
 import confidence_scheduled_ragged_amd as dspark  # noqa: F401
+import forward_ref as ref
 from test_gpu_attention import DEV, SCALES, call, make, pools
 
 pytestmark = pytest.mark.gpu
@@ -106,3 +107,24 @@ def test_every_row_of_a_tile_seen_in_part(D, cache, keys, rows):
         assert bool(got[sees][:, :, ::5].isnan().all()), at
         got[sees] = torch.where(got[sees].isnan(), clean[sees], got[sees])
         assert torch.equal(got, clean), at
+
+
+@pytest.mark.parametrize("D", [64, 128, 96, 136, 192])
+@pytest.mark.parametrize("rows,ctx", [([1], [4000]), ([17, 1], [300, 5]), ([150], [40])])
+def test_scores_of_minus_infinity_weigh_nothing(D, rows, ctx):
+    """Against a key so low that its weight is 0 in 64 bits (exp(-250)) and, where
+    every position scores -inf, against zeros."""
+    c = make(rows, ctx, 8, 2, D, 16, seed=35)
+    c["q"][:, :, 7] = 1.0
+    hit = [t for t in range(ctx[0] + rows[0]) if t % 3 == 1]
+    poison(c, "kc", 0, hit, -4000.0, slice(7, 8))
+    out = torch.zeros((c["cap"], 8, D), dtype=torch.bfloat16)
+    want, tol = ref.attend(c["q"], c["kc"], c["vc"], c["cu"], c["ctx"], c["table"],
+                           c["max_rows"], out=out)
+    poison(c, "kc", 0, hit, -INF, slice(7, 8))
+    got = run(c, "bf16").double()
+    assert bool(((got - want).abs() <= tol).all())
+    poison(c, "kc", 0, range(ctx[0] + rows[0]), -INF, slice(7, 8))
+    got = run(c, "bf16").double()
+    assert float(got[:rows[0]].abs().max()) == 0.0
+    assert bool(((got - want).abs() <= tol)[rows[0]:].all())
