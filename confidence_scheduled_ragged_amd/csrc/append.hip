@@ -5,8 +5,10 @@
 //   y1 = x1 cos(p, i) - x2 sin(p, i),   y2 = x2 cos(p, i) + x1 sin(p, i)
 // in fp32, rounded once. Each input is read once and each output written once,
 // so HBM bytes bound the call (and the launch, for a few rows): 11624 prompt tokens
-// of 16 + 4 heads into an 8-bit cache, 134 MB, take 23.9 us (5.6 TB/s), a mixed batch
-// of 256 requests, 49 MB, 10.8 us (4.5 TB/s), one row 3.3 us.
+// of 16 + 4 heads into an 8-bit cache, 134 MB, take 30 us where the tensors change
+// from call to call (4.5 TB/s) and 24 us where they stay the same and partly in the
+// 256 MB last-level cache (5.6 TB/s); a mixed batch of 256 requests, 49 MB, 10.5 us
+// (4.6 TB/s), one row 3.2 us.
 #include "forward.hpp"
 
 namespace dspark {

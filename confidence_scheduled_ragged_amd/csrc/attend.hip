@@ -145,14 +145,19 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
 // whatever unit they belong to. Through registers, the loads alone took 326 of the
 // 409 us of a mixed batch (256 requests, 1.33 GB of keys and values) and 405 of the
 // 831 us of a prompt's chunk (2048 rows on 14000 positions). Calls of up to 128 query
-// rows a head (decoding, verify windows) are bound by HBM: two workgroups of four
-// waves a CU, a tile at work and one on its way in each. The mixed batch takes 297
-// us, 4.5 TB/s; four contexts of 40000 to 120000 in 8 bits 143 us, 4.5 TB/s; one
-// token at 4000, bound by a chain of some ten round trips to memory, 21 us. Calls
-// with more (prompts) are bound by the matrix and vector instructions of the
-// softmax, which two waves of a SIMD overlap poorly: one workgroup of eight waves a
-// CU, four tiles in LDS, so that keys are read from L2 once for 256 rows. The chunk
-// takes 583 us, 865 TFLOP/s; four prompts of 1882 to 2902 tokens 312 us, 671 TFLOP/s.
+// rows a head (decoding, verify windows) have two workgroups of four waves a CU, a
+// tile at work and one on its way in each. The mixed batch takes 302 us, 4.4 TB/s
+// (its loads alone 242 us, 5.5 TB/s: the products, and units that begin and end, are
+// not all behind them); four contexts of 40000 to 120000 in 8 bits 147 us, 4.4 TB/s
+// (loads alone 137 us, 4.7 TB/s, by what two tiles keep on their way); one token at
+// 4000, a chain of some ten round trips to memory, 21 us (14). Calls with more
+// (prompts) are bound by the matrix and vector instructions of the softmax, which
+// two waves of a SIMD overlap poorly: one workgroup of eight waves a CU, four tiles in
+// LDS, so that keys are read from L2 once for 256 rows. The chunk takes 602 us, 837
+// TFLOP/s (loads alone 199 us), four prompts of 1882 to 2902 tokens 312 us, 671
+// TFLOP/s (99 us); in 8 bits these prompts take 347 us, since that kernel spills 25
+// registers, whose reloads wait behind the loads into LDS. Figures of one card;
+// others took 1 to 5 % more or less.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds 16 of a query's 32
 // scores of one MFMA (the other 16 sit in lane ^ 32), so the softmax needs one
@@ -1328,7 +1333,18 @@ static int tile_wgs(bool wide) { return device_cu_count() * (wide ? 1 : 2); }
 // Calls whose requests may have over 128 query rows of a key-value head (prompts)
 // take blocks of 256, eight waves of 32 rows against all keys of a tile: the keys
 // are read from L2 half as often. Others share a tile's keys out to the waves. One
-// kernel for both spilled its registers.
+// kernel for both spilled its registers. Measured on either side, us in blocks of 256
+// and of 128 (256 requests at 128 to 4096 with groups of 8, but for the prompts):
+//   windows of 32, all whole (256 rows)     514 and 654, e4m3  534 and 604
+//   windows of 64, all whole                998 and 1237       1044 and 1154
+//   windows of up to 17 (136), ragged       437 and 417        524 and 359
+//   windows of up to 64, ragged             628 and 625        722 and 598
+//   4 prompts of 256, 1024 and 4096 rows    38, 95, 721 and 39, 103, 837
+//                                    e4m3   38, 102, 752 and 31, 108, 855
+//   2048 rows on 14000                      601 and 717
+//     packed with 64, 256 tokens at 2000    742, 1253 and 831, 1120 (groups of 4)
+// So the rule serves whole windows and prompts; where most of a call's requests have
+// few rows, one of eight waves works for each, and ragged 8-bit windows pay most.
 static bool tile_wide(int max_rows, int Hq, int Hkv) {
     return (int64_t)max_rows * (Hq / Hkv) > kNarrowRows;
 }
