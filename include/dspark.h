@@ -443,7 +443,8 @@ dspark_status dspark_append_kv(const dspark_bf16 *q, const dspark_bf16 *k, const
  * bytes (e4m3 caches to 8), else DSPARK_ERR_ALIGN. ws: at least
  * dspark_attention_workspace_bytes(...) bytes, 16-byte aligned, zero-filled
  * before its first use (dspark_workspace_init), shared by no two calls that
- * overlap in time. Other checks as for dspark_append_kv, and DSPARK_ERR_ARG for
+ * overlap in time and not with other entry points, whose words lie elsewhere in
+ * theirs. Other checks as for dspark_append_kv, and DSPARK_ERR_ARG for
  * a scale that is not finite or a negative window.
  */
 dspark_status dspark_verify_attention(const dspark_bf16 *q, long long q_row, long long q_head,
