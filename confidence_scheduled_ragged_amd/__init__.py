@@ -70,13 +70,26 @@ def lib() -> ctypes.CDLL:
         L.dspark_attention_workspace_bytes.argtypes = [I, I, I, I, I]
         L.dspark_attention_workspace_bytes.restype = S
         L.dspark_sample_accept.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, P, P, P, P, S, P]
+        L.dspark_tree_masks.argtypes = [P, P, P, I, I, I, I, I, I, P, P, P]
+        L.dspark_append_tree_kv.argtypes = (L.dspark_append_kv.argtypes[:11] + [P]
+                                            + L.dspark_append_kv.argtypes[11:])
+        L.dspark_tree_attention.argtypes = (L.dspark_verify_attention.argtypes[:24]
+                                            + [I, P, P, I] + L.dspark_verify_attention.argtypes[24:])
+        L.dspark_tree_accept.argtypes = [P, P, P, P, I, I, I, I, P, P, P, P]
+        L.dspark_move_kv.argtypes = [P, P, I, I, LL, I, I, LL, LL, LL, I, I, P, P, I, P, P, I, I, P]
+        L.dspark_resize_pages.argtypes = [P, P, P, I, I, I, P, I, P, P]
+        L.dspark_fork_pages.argtypes = [P, P, P, I, I, I, P, I, P, P, I, P, P, P, P, P]
+        L.dspark_copy_pages.argtypes = [P, P, I, I, LL, I, I, LL, LL, LL, I, I, P, P, P, I, P]
         L.dspark_status_string.argtypes = [I]
         L.dspark_status_string.restype = ctypes.c_char_p
         for f in (L.dspark_confidence, L.dspark_schedule, L.dspark_compact, L.dspark_accept,
                   L.dspark_step, L.dspark_workspace_init, L.dspark_cap_accept,
                   L.dspark_gather_rows, L.dspark_tier_select, L.dspark_cost_cutoff,
                   L.dspark_step_ex, L.dspark_step_status, L.dspark_step_noalloc,
-                  L.dspark_append_kv, L.dspark_verify_attention, L.dspark_sample_accept):
+                  L.dspark_append_kv, L.dspark_verify_attention, L.dspark_sample_accept,
+                  L.dspark_tree_masks, L.dspark_append_tree_kv, L.dspark_tree_attention,
+                  L.dspark_tree_accept, L.dspark_move_kv, L.dspark_resize_pages,
+                  L.dspark_fork_pages, L.dspark_copy_pages):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -115,6 +128,18 @@ def _stream(device: torch.device):
 def _raw_stream(index: int) -> int:
     """The current stream's handle without a Stream object in between."""
     return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _launch(gpu: int, name: str, *args) -> None:
+    """Calls an entry point on GPU `gpu`, which need not be the current one."""
+    fn = getattr(lib(), name)
+    if torch.cuda.device_count() > 1:
+        with torch.cuda.device(gpu):
+            status = fn(*args, _raw_stream(gpu))
+    else:
+        status = fn(*args, _raw_stream(gpu))
+    if status:
+        _ok(name, status)
 
 
 def _ok(fn: str, status: int):
@@ -631,6 +656,13 @@ def dspark_append_kv(q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cac
     heads side by side), cos and sin [positions, rot / 2] fp32, ctx_lens [B]
     tokens cached before the call, block_table [B, width] int32, k_cache and
     v_cache [pages, Hkv, page_size, D] bf16 or float8_e4m3fn."""
+    return _append("dspark_append_kv", (), q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table,
+                   k_cache, v_cache, interleaved, k_scale, v_scale, out)
+
+
+def _append(name, depths, q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cache, v_cache,
+            interleaved, k_scale, v_scale, out):
+    """dspark_append_kv, or with (depths,) dspark_append_tree_kv."""
     gpu, B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(
         k_cache, v_cache, cu_seqlens, ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
@@ -644,17 +676,19 @@ def dspark_append_kv(q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cac
     _need(sin, "sin", torch.float32, angles, gpu)
     if len(angles) != 2:
         raise ValueError("cos must have shape (positions, rotated pairs)")
+    for t in depths:
+        _need(t, "depths", torch.int32, (rows,), gpu)
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
-    status = lib().dspark_append_kv(
+    _launch(
+        gpu, name,
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], ks[0], vs[0], cos.data_ptr(),
-        sin.data_ptr(), angles[0], angles[1], 1 if interleaved else 0, cu_seqlens.data_ptr(),
+        sin.data_ptr(), angles[0], angles[1], 1 if interleaved else 0,
+        *[t.data_ptr() for t in depths], cu_seqlens.data_ptr(),
         ctx_lens.data_ptr(), B, rows, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), kind,
         pages, page, ps, hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
-        out.data_ptr(), _raw_stream(gpu))
-    if status:
-        _ok("dspark_append_kv", status)
+        out.data_ptr())
     return out
 
 
@@ -685,6 +719,13 @@ def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_tab
     scale defaults to D ** -0.5. Returns out [rows, Hq, D] bf16. Without ws the
     call uses attention_workspace(), one for all streams of the GPU: calls on
     several streams at a time need one each."""
+    return _attend("dspark_verify_attention", None, q, k_cache, v_cache, cu_seqlens, ctx_lens,
+                   block_table, max_rows, window, scale, k_scale, v_scale, out, ws)
+
+
+def _attend(name, tree, q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, max_rows, window,
+            scale, k_scale, v_scale, out, ws):
+    """dspark_verify_attention, or with (depths, masks, sinks) dspark_tree_attention."""
     gpu, B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(
         k_cache, v_cache, cu_seqlens, ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
@@ -693,18 +734,29 @@ def dspark_verify_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_tab
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
     max_rows = min(int(max_rows), rows)
+    view = ()
+    if tree is not None:
+        depths, masks, sinks = tree
+        if (depths is None) != (masks is None):
+            raise ValueError("depths and masks must be given together")
+        if masks is None:
+            view = (int(sinks), None, None, 0)
+        else:
+            _need(depths, "depths", torch.int32, (rows,), gpu)
+            _need(masks, "masks", torch.int32, None, gpu)
+            if masks.dim() != 2 or masks.shape[0] != rows:
+                raise ValueError(f"masks must have shape ({rows}, words)")
+            view = (int(sinks), depths.data_ptr(), masks.data_ptr(), masks.shape[1])
     if ws is None:
         ws = attention_workspace(B, max_rows, Hq, Hkv, D, q.device)
     else:
         _need(ws, "ws", torch.uint8, None, gpu)
-    status = lib().dspark_verify_attention(
+    _launch(
+        gpu, name,
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), kind, pages, page, ps,
         hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
         cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, rows, max_rows, Hq, Hkv, D, int(window),
-        D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
-        _raw_stream(gpu))
-    if status:
-        _ok("dspark_verify_attention", status)
+        *view, D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -756,11 +808,206 @@ def dspark_sample_accept(logits, packed_src_row, cu_seqlens, tokens, uniforms, t
     return smp, acc, bon
 
 
+# --------------------------------------------- drafted trees and shared pages
+
+def dspark_tree_masks(parents, cu_seqlens, max_rows, ctx_lens=None, window=0, sinks=0, out=None):
+    """(depths [rows], masks [rows, words]) int32 of drafted trees: parents [rows]
+    int32, the place of each row's parent among its request's rows (below its own;
+    anything else is a root), max_rows the most rows of a request, words as many as
+    hold that many bits. ctx_lens [B] is needed with window and sinks. Rows past
+    cu_seqlens[-1] are untouched."""
+    _need(parents, "parents", torch.int32)
+    gpu, rows = parents.get_device(), parents.numel()
+    _need(cu_seqlens, "cu_seqlens", torch.int32, None, gpu)
+    B = cu_seqlens.numel() - 1
+    if ctx_lens is not None:
+        _need(ctx_lens, "ctx_lens", torch.int32, (B,), gpu)
+    elif window > 0 and sinks > 0:
+        raise ValueError("ctx_lens must be given with window and sinks")
+    words = -(-int(max_rows) // 32)
+    depths, masks = (None, None) if out is None else out
+    if depths is None:
+        depths = torch.zeros(rows, dtype=torch.int32, device=parents.device)
+    if masks is None:
+        masks = torch.zeros((rows, max(words, 1)), dtype=torch.int32, device=parents.device)
+    _need(depths, "depths", torch.int32, (rows,), gpu)
+    _need(masks, "masks", torch.int32, None, gpu)
+    if masks.dim() != 2 or masks.shape[0] != rows:
+        raise ValueError(f"masks must have shape ({rows}, words)")
+    _launch(
+        gpu, "dspark_tree_masks",
+        parents.data_ptr(), cu_seqlens.data_ptr(), None if ctx_lens is None else ctx_lens.data_ptr(),
+        B, rows, int(max_rows), int(window), int(sinks), masks.shape[1], depths.data_ptr(),
+        masks.data_ptr())
+    return depths, masks
+
+
+def dspark_append_tree_kv(q, k, v, cos, sin, depths, cu_seqlens, ctx_lens, block_table, k_cache,
+                          v_cache, interleaved=False, k_scale=1.0, v_scale=1.0, out=None):
+    """dspark_append_kv for the nodes of trees: a row is rotated by the position
+    ctx_lens[b] + depths[row] (dspark_tree_masks) and keeps the slot that it has in a
+    chain. Returns the rotated queries."""
+    return _append("dspark_append_tree_kv", (depths,), q, k, v, cos, sin, cu_seqlens, ctx_lens,
+                   block_table, k_cache, v_cache, interleaved, k_scale, v_scale, out)
+
+
+def dspark_tree_attention(q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, max_rows,
+                          depths=None, masks=None, window=0, sinks=0, scale=None, k_scale=1.0,
+                          v_scale=1.0, out=None, ws=None):
+    """dspark_verify_attention for the nodes of trees (depths [rows] and masks [rows,
+    words] int32 of dspark_tree_masks; none for a chain), and with the first `sinks`
+    positions visible beside a window. Without ws the call uses
+    attention_workspace(), as dspark_verify_attention does."""
+    return _attend("dspark_tree_attention", (depths, masks, sinks), q, k_cache, v_cache,
+                   cu_seqlens, ctx_lens, block_table, max_rows, window, scale, k_scale, v_scale,
+                   out, ws)
+
+
+def dspark_tree_accept(packed_choice, packed_tokens, parents, cu_seqlens, max_rows, width, out=None):
+    """(accepted [B], bonus [B], path [B, width]) int32: the walk down every request's
+    tree by the target's choices (packed_argmax of dspark_accept or packed_sample of
+    dspark_sample_accept). path holds places among the request's rows, from row 0 on,
+    then -1; at most width - 1 drafts are accepted."""
+    _need(packed_choice, "packed_choice", torch.int32)
+    gpu, rows, dev = packed_choice.get_device(), packed_choice.numel(), packed_choice.device
+    _need(packed_tokens, "packed_tokens", torch.int32, None, gpu)
+    _need(parents, "parents", torch.int32, None, gpu)
+    if packed_tokens.numel() != rows or parents.numel() != rows:
+        raise ValueError("packed_choice, packed_tokens and parents must have one entry a row")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, None, gpu)
+    B = cu_seqlens.numel() - 1
+    acc, bonus, path = (None, None, None) if out is None else out
+    acc = torch.empty(B, dtype=torch.int32, device=dev) if acc is None else acc
+    bonus = torch.empty(B, dtype=torch.int32, device=dev) if bonus is None else bonus
+    path = torch.empty((B, width), dtype=torch.int32, device=dev) if path is None else path
+    _need(acc, "accepted", torch.int32, (B,), gpu)
+    _need(bonus, "bonus", torch.int32, (B,), gpu)
+    _need(path, "path", torch.int32, (B, width), gpu)
+    _launch(
+        gpu, "dspark_tree_accept",
+        packed_choice.data_ptr(), packed_tokens.data_ptr(), parents.data_ptr(),
+        cu_seqlens.data_ptr(), B, rows, int(max_rows), int(width), acc.data_ptr(),
+        bonus.data_ptr(), path.data_ptr())
+    return acc, bonus, path
+
+
+def _layered(k_cache, v_cache):
+    """Checks pools [layers, pages, Hkv, page_size, D] or [pages, Hkv, page_size, D];
+    returns their GPU and the arguments from the pointers to D."""
+    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if len(shape) not in (4, 5) or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have one shape, [layers, pages, Hkv, page_size, "
+                         "D] or [pages, Hkv, page_size, D]")
+    gpu = k_cache.get_device()
+    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.get_device() != gpu:
+        raise ValueError(f"the caches must be on one GPU (got {k_cache.device}, {v_cache.device})")
+    if dtype not in _CACHE_TYPES or v_cache.dtype is not dtype:
+        raise TypeError(f"the caches must be bfloat16 or float8_e4m3fn (got {dtype}, "
+                        f"{v_cache.dtype})")
+    if v_cache.stride() != strides or strides[-1] != 1:
+        raise ValueError("k_cache and v_cache must share strides, with D contiguous")
+    layers, layer_stride = (shape[0], strides[0]) if len(shape) == 5 else (1, 0)
+    pages, Hkv, page, D = shape[-4:]
+    ps, hs, ss = strides[-4:-1]
+    return gpu, (k_cache.data_ptr(), v_cache.data_ptr(), _CACHE_TYPES[dtype], layers, layer_stride,
+                 pages, page, ps, hs, ss, Hkv, D)
+
+
+def dspark_move_kv(k_cache, v_cache, path, accepted, ctx_lens, block_table):
+    """Brings every request's accepted path (dspark_tree_accept) together in the
+    cache: slot ctx_lens[b] + path[b, i] goes to slot ctx_lens[b] + i, keys and values.
+    The caches are those of all layers, [layers, pages, Hkv, page_size, D], or of one."""
+    gpu, pool = _layered(k_cache, v_cache)
+    _need(path, "path", torch.int32, None, gpu)
+    if path.dim() != 2:
+        raise ValueError("path must have shape (B, width)")
+    B, width = path.shape
+    _need(accepted, "accepted", torch.int32, (B,), gpu)
+    _need(ctx_lens, "ctx_lens", torch.int32, (B,), gpu)
+    _need(block_table, "block_table", torch.int32, None, gpu)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, pages of a request)")
+    _launch(gpu, "dspark_move_kv", *pool, path.data_ptr(), accepted.data_ptr(), width,
+            ctx_lens.data_ptr(), block_table.data_ptr(), block_table.shape[1], B)
+
+
+def page_pool(pages: int, rows: int, width: int, device):
+    """(table [rows, width], held [rows], refs [pages]) of a new pool: no row holds a page."""
+    table = torch.full((rows, width), -1, dtype=torch.int32, device=device)
+    return table, torch.zeros(rows, dtype=torch.int32, device=device), torch.zeros(
+        pages, dtype=torch.int32, device=device)
+
+
+def _pool(table, held, refs, lens):
+    _need(table, "table", torch.int32)
+    if table.dim() != 2:
+        raise ValueError("table must have shape (rows, pages of a row)")
+    gpu, (R, width) = table.get_device(), table.shape
+    _need(held, "held", torch.int32, (R,), gpu)
+    _need(refs, "refs", torch.int32, None, gpu)
+    _need(lens, "lens", torch.int32, (R,), gpu)
+    return gpu, R, width
+
+
+def dspark_resize_pages(table, held, refs, lens, page_size, granted=None):
+    """Every row of the table [R, width] gets and gives back pages until it holds
+    ceil(lens[b] / page_size) of them (page_pool() makes the state: table, held [R],
+    refs [pages], all changed in place). Returns granted [R] int32: 1 where the row
+    holds what its length needs, 0 where there were too few free pages or places."""
+    gpu, R, width = _pool(table, held, refs, lens)
+    granted = torch.empty_like(held) if granted is None else granted
+    _need(granted, "granted", torch.int32, (R,), gpu)
+    _launch(gpu, "dspark_resize_pages", table.data_ptr(), held.data_ptr(), lens.data_ptr(), R,
+            width, int(page_size), refs.data_ptr(), refs.numel(), granted.data_ptr())
+    return granted
+
+
+def dspark_fork_pages(table, held, refs, src, dst, lens, page_size, out=None):
+    """Row dst[i] becomes a copy of row src[i] up to position lens[src[i]]: full pages
+    are shared, and where the positions end inside a page the row gets one of its own.
+    Returns (copy_src, copy_dst, copy_slots, granted) [n] int32; the first three are
+    what dspark_copy_pages takes to fill those pages. Rows that cannot be served have
+    granted 0 and stay as they were."""
+    gpu, R, width = _pool(table, held, refs, lens)
+    _need(src, "src", torch.int32, None, gpu)
+    n = src.numel()
+    _need(dst, "dst", torch.int32, (n,), gpu)
+    _need(src, "src", torch.int32, (n,), gpu)
+    if out is None:
+        out = tuple(torch.empty_like(src) for _ in range(4))
+    for t, name in zip(out, ("copy_src", "copy_dst", "copy_slots", "granted")):
+        _need(t, name, torch.int32, (n,), gpu)
+    _launch(
+        gpu, "dspark_fork_pages",
+        table.data_ptr(), held.data_ptr(), lens.data_ptr(), R, width, int(page_size),
+        refs.data_ptr(), refs.numel(), src.data_ptr(), dst.data_ptr(), n,
+        *[t.data_ptr() for t in out])
+    return out
+
+
+def dspark_copy_pages(k_cache, v_cache, src, dst, slots=None):
+    """Copies the first slots[i] slots (None: all) of page src[i] to page dst[i], keys
+    and values, in the caches of all layers or of one; entries outside the pool copy
+    nothing."""
+    gpu, pool = _layered(k_cache, v_cache)
+    _need(src, "src", torch.int32, None, gpu)
+    n = src.numel()
+    _need(src, "src", torch.int32, (n,), gpu)
+    _need(dst, "dst", torch.int32, (n,), gpu)
+    if slots is not None:
+        _need(slots, "slots", torch.int32, (n,), gpu)
+    _launch(gpu, "dspark_copy_pages", *pool, src.data_ptr(), dst.data_ptr(),
+            None if slots is None else slots.data_ptr(), n)
+
+
 __all__ = ["DsparkError", "lib", "LIB_PATH", "dspark_status_string", "dspark_confidence", "dspark_schedule",
            "dspark_compact", "dspark_accept", "dspark_step", "dspark_cap_accept",
            "dspark_gather_rows", "dspark_tier_select", "dspark_cost_cutoff",
            "dspark_step_ex", "dspark_step_status", "dspark_step_noalloc", "BoundStep", "bind_step",
            "dspark_append_kv", "dspark_verify_attention", "dspark_sample_accept",
+           "dspark_tree_masks", "dspark_append_tree_kv", "dspark_tree_attention",
+           "dspark_tree_accept", "dspark_move_kv", "dspark_resize_pages", "dspark_fork_pages",
+           "dspark_copy_pages", "page_pool",
            "dspark_attention_workspace_bytes", "attention_workspace", "dspark_workspace_bytes",
            "dspark_workspace_init", "workspace", "alloc_step_outputs", "STEP_OUTPUTS",
            "DSPARK_CUT_THRESHOLD", "DSPARK_CUT_BUDGET", "DSPARK_CUT_STATIC",

@@ -51,13 +51,29 @@ __device__ __forceinline__ void store1(void *pool, int64_t at, float x, float sc
         static_cast<uint16_t *>(pool)[at] = (uint16_t)pack_bf16(x, 0.f);
 }
 
+// Where row j of a request stands: its position, which its angles come from, and the
+// element offset of its slot. In a chain the slot is the position's; a node of a tree
+// keeps its row's slot and stands as deep below the context as its ancestors are.
+struct Place {
+    int64_t pos, slot;
+};
+template <bool kTree>
+__device__ __forceinline__ Place place_of(const AppendParams &p, int b, int r, int j) {
+    const int64_t ctx = p.ctx[b] < 0 ? 0 : p.ctx[b];
+    const int32_t *row = p.c.table + (int64_t)b * p.c.table_width;
+    Place at;
+    at.pos = ctx + (kTree ? depth_of(p.depths, r, j) : j);
+    at.slot = ctx + j > 0x7FFFFFFF ? -1 : slot_offset(p.c, row, (int)(ctx + j), 0);
+    return at;
+}
+
 // One wave takes `heads_per` heads of a packed row at a time: with D/16 items
 // of 16 elements per head, a lane keeps one item's cosines and sines in
 // registers for every head it visits (the table is read once per wave and not
 // once per head). An item is two groups of 8: the two halves of 8 rotated
 // pairs (first half i, second half i, or adjacent pairs when interleaved), or
 // 16 elements that are not rotated. `split` waves share a row.
-template <bool kE4m3, bool kInterleaved>
+template <bool kE4m3, bool kInterleaved, bool kTree>
 __global__ __launch_bounds__(kAppendThreads) void append_vec_kernel(AppendParams p, int split) {
     const int lane = threadIdx.x & (kWave - 1);
     const int w = blockIdx.x * (kAppendThreads / kWave) + threadIdx.x / kWave;
@@ -66,9 +82,10 @@ __global__ __launch_bounds__(kAppendThreads) void append_vec_kernel(AppendParams
     const int b = wave_request_of(p.cu, p.B, r);
     if (b >= p.B) return;
     const int j = r - p.cu[b];
-    const int64_t at_pos = (int64_t)(p.ctx[b] < 0 ? 0 : p.ctx[b]) + j;
-    if (j < 0 || at_pos >= p.positions) return;
-    const int pos = (int)at_pos;
+    if (j < 0) return;
+    const Place at = place_of<kTree>(p, b, r, j);
+    if (at.pos >= p.positions) return;
+    const int pos = (int)at.pos;
 
     const int items = p.D / 16, per = kWave / items;
     const int hl = lane / items, it = lane - hl * items;
@@ -90,7 +107,7 @@ __global__ __launch_bounds__(kAppendThreads) void append_vec_kernel(AppendParams
             s[4 + i] = s1[i];
         }
     }
-    const int64_t slot = slot_offset(p.c, p.c.table + (int64_t)b * p.c.table_width, pos, 0);
+    const int64_t slot = at.slot;
     const int heads = p.Hq + 2 * p.Hkv;
 #pragma unroll 2
     for (int h = part * per + hl; h < heads; h += split * per) {
@@ -140,7 +157,7 @@ __global__ __launch_bounds__(kAppendThreads) void append_vec_kernel(AppendParams
 
 // Any head size, stride and alignment: one wave per packed row, one pair or one
 // element per lane at a time (the mixed batch: 42 us).
-template <bool kE4m3, bool kInterleaved>
+template <bool kE4m3, bool kInterleaved, bool kTree>
 __global__ __launch_bounds__(kAppendThreads) void append_any_kernel(AppendParams p) {
     const int lane = threadIdx.x & (kWave - 1);
     const int r = blockIdx.x * (kAppendThreads / kWave) + threadIdx.x / kWave;
@@ -148,10 +165,11 @@ __global__ __launch_bounds__(kAppendThreads) void append_any_kernel(AppendParams
     const int b = wave_request_of(p.cu, p.B, r);
     if (b >= p.B) return;
     const int j = r - p.cu[b];
-    const int64_t at_pos = (int64_t)(p.ctx[b] < 0 ? 0 : p.ctx[b]) + j;
-    if (j < 0 || at_pos >= p.positions) return;
-    const int pos = (int)at_pos;
-    const int64_t slot = slot_offset(p.c, p.c.table + (int64_t)b * p.c.table_width, pos, 0);
+    if (j < 0) return;
+    const Place at = place_of<kTree>(p, b, r, j);
+    if (at.pos >= p.positions) return;
+    const int pos = (int)at.pos;
+    const int64_t slot = at.slot;
     const int heads = p.Hq + 2 * p.Hkv, half = p.half, rest = p.D - 2 * half;
     const int per_head = half + rest;  // pairs, then single elements
     auto put = [&](int h, int e, float x) {
@@ -188,7 +206,7 @@ __global__ __launch_bounds__(kAppendThreads) void append_any_kernel(AppendParams
     }
 }
 
-template <bool kE4m3, bool kInterleaved>
+template <bool kE4m3, bool kInterleaved, bool kTree>
 static hipError_t launch_append_t(const AppendParams &p, hipStream_t s) {
     const int wpb = kAppendThreads / kWave;
     const int64_t item = kE4m3 ? 1 : 2;
@@ -201,7 +219,7 @@ static hipError_t launch_append_t(const AppendParams &p, hipStream_t s) {
     for (const void *x : a16) vec = vec && (uintptr_t)x % 16 == 0;
     vec = vec && (uintptr_t)p.c.k % (8 * item) == 0 && (uintptr_t)p.c.v % (8 * item) == 0;
     if (!vec) {
-        hipLaunchKernelGGL((append_any_kernel<kE4m3, kInterleaved>),
+        hipLaunchKernelGGL((append_any_kernel<kE4m3, kInterleaved, kTree>),
                            dim3((p.rows + wpb - 1) / wpb), dim3(kAppendThreads), 0, s, p);
         return hipGetLastError();
     }
@@ -213,16 +231,24 @@ static hipError_t launch_append_t(const AppendParams &p, hipStream_t s) {
     while (split < most && (int64_t)p.rows * split < 4096) split *= 2;
     if (split > most) split = most;
     const int64_t waves = (int64_t)p.rows * split;
-    hipLaunchKernelGGL((append_vec_kernel<kE4m3, kInterleaved>),
+    hipLaunchKernelGGL((append_vec_kernel<kE4m3, kInterleaved, kTree>),
                        dim3((unsigned)((waves + wpb - 1) / wpb)), dim3(kAppendThreads), 0, s, p,
                        split);
     return hipGetLastError();
 }
 
-hipError_t launch_append_kv(const AppendParams &p, bool interleaved, bool e4m3, hipStream_t s) {
+template <bool kTree>
+static hipError_t launch_append(const AppendParams &p, bool interleaved, bool e4m3, hipStream_t s) {
     if (e4m3)
-        return interleaved ? launch_append_t<true, true>(p, s) : launch_append_t<true, false>(p, s);
-    return interleaved ? launch_append_t<false, true>(p, s) : launch_append_t<false, false>(p, s);
+        return interleaved ? launch_append_t<true, true, kTree>(p, s)
+                           : launch_append_t<true, false, kTree>(p, s);
+    return interleaved ? launch_append_t<false, true, kTree>(p, s)
+                       : launch_append_t<false, false, kTree>(p, s);
+}
+
+hipError_t launch_append_kv(const AppendParams &p, bool interleaved, bool e4m3, hipStream_t s) {
+    return p.depths ? launch_append<true>(p, interleaved, e4m3, s)
+                    : launch_append<false>(p, interleaved, e4m3, s);
 }
 
 }  // namespace dspark

@@ -56,9 +56,9 @@ __device__ __forceinline__ float load1(const void *pool, int64_t at) {
 // time, a lane per key for the scores and a lane per output element for the
 // weighted values. Bound by its latency: 32 requests of mixed traffic at D = 96 took
 // 2127 us here and take 66 us in the tiles below, so only heads over 128 and pools
-// that 16-byte loads do not fit come here.
-template <bool kE4m3>
-__global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p) {
+// that 16-byte loads do not fit come here. kTree: the rows that TreeView describes.
+template <bool kE4m3, bool kTree>
+__global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p, TreeView v) {
     __shared__ float q_s[kMaxHeadDim];
     __shared__ float p_s[kWave];
     __shared__ int64_t at_s[kWave];
@@ -66,23 +66,37 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
     const int r = blockIdx.x, h = blockIdx.y;
     const int b = wave_request_of(p.cu, p.B, r);
     if (b >= p.B) return;
-    const int j = r - p.cu[b];
+    const int first = p.cu[b], j = r - first;
     if (j < 0 || j >= p.max_rows) return;
     const int kvh = h / (p.Hq / p.Hkv);
+    const bool masked = kTree && v.masks;
     // positions past the table's width have no page
     const int64_t width = (int64_t)p.c.table_width * p.c.page;
-    const int64_t pos = (int64_t)context_of(p.ctx[b]) + j;
-    const int64_t end = pos + 1 < width ? pos + 1 : width;
-    const int64_t begin = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
+    const int64_t ctx = context_of(p.ctx[b]);
+    const int64_t pos = ctx + (masked ? depth_of(v.depths, r, j) : j);
+    int64_t last = pos + 1;  // and the first position in the window
+    int64_t begin = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
+    const uint32_t *mask = nullptr;
+    if (masked) {
+        const int rows = p.cu[b + 1] < p.rows ? p.cu[b + 1] - first : p.rows - first;
+        last = ctx + (rows < p.max_rows ? rows : p.max_rows);
+        begin = begin < ctx ? begin : ctx;
+        mask = v.masks + (int64_t)r * v.words;
+    }
+    const int64_t end = last < width ? last : width;
+    const int64_t sinks = !kTree ? 0 : (v.sinks < begin ? v.sinks : begin);
+    const int64_t sinks_end = sinks < width ? sinks : width;
     const int32_t *row = p.c.table + (int64_t)b * p.c.table_width;
     const uint16_t *q = p.q + r * p.q_row + h * p.q_head;
     for (int d = lane; d < p.D; d += kWave) q_s[d] = bf16_f32(q[d]) * p.scale * p.c.k_scale;
     __syncthreads();
     float m = -INFINITY, total = 0.f;
     float acc[kMaxHeadDim / kWave] = {};
-    for (int64_t t0 = begin; t0 < end; t0 += kWave) {
+    auto keys = [&](int64_t t0, int64_t t1) {
         const int64_t t = t0 + lane;
-        const int64_t at = t < end ? slot_offset(p.c, row, (int)t, kvh) : -1;
+        bool see = t < t1;
+        if (masked && see && t >= ctx) see = mask[(t - ctx) >> 5] >> ((t - ctx) & 31) & 1;
+        const int64_t at = see ? slot_offset(p.c, row, (int)t, kvh) : -1;
         float x = -INFINITY;
         if (at >= 0) {
             x = 0.f;
@@ -97,7 +111,7 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
 #pragma unroll
         for (int off = kWave / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
         // fmaxf drops NaN: keys may be there that leave no maximum
-        if (!__any(at >= 0)) continue;
+        if (!__any(at >= 0)) return;
         const float m1 = fmaxf(m, top);
         const float base = m1 == -INFINITY ? 0.f : m1;
         const float keep = expf(m - base);  // 0 before the first maximum
@@ -118,7 +132,9 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p)
             }
         }
         __syncthreads();
-    }
+    };
+    for (int64_t t = 0; t < sinks_end; t += kWave) keys(t, sinks_end);
+    for (int64_t t = begin; t < end; t += kWave) keys(t, end);
     uint16_t *o = p.out + ((int64_t)r * p.Hq + h) * p.D;
     const float norm = total > 0.f ? p.c.v_scale / total : 0.f;
 #pragma unroll
@@ -1414,6 +1430,16 @@ static hipError_t launch_tiles(const AttendParams &p, void *ws, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <bool kTree>
+static hipError_t launch_rows(const AttendParams &p, const TreeView &v, bool e4m3, hipStream_t s) {
+    const dim3 grid((unsigned)p.rows, (unsigned)p.Hq);
+    if (e4m3)
+        hipLaunchKernelGGL((attend_row_kernel<true, kTree>), grid, dim3(kRowThreads), 0, s, p, v);
+    else
+        hipLaunchKernelGGL((attend_row_kernel<false, kTree>), grid, dim3(kRowThreads), 0, s, p, v);
+    return hipGetLastError();
+}
+
 hipError_t launch_attention(const AttendParams &p, bool e4m3, void *ws, hipStream_t s) {
     // an 8-bit cache may be aligned to 8 bytes only
     const bool aligned = (((uintptr_t)p.c.k | (uintptr_t)p.c.v) % 16 == 0) &&
@@ -1424,10 +1450,13 @@ hipError_t launch_attention(const AttendParams &p, bool e4m3, void *ws, hipStrea
     case 64:
         return e4m3 ? launch_tiles<64, true>(p, ws, s) : launch_tiles<64, false>(p, ws, s);
     }
-    const dim3 grid((unsigned)p.rows, (unsigned)p.Hq);
-    if (e4m3) hipLaunchKernelGGL((attend_row_kernel<true>), grid, dim3(kRowThreads), 0, s, p);
-    else hipLaunchKernelGGL((attend_row_kernel<false>), grid, dim3(kRowThreads), 0, s, p);
-    return hipGetLastError();
+    return launch_rows<false>(p, TreeView{}, e4m3, s);
+}
+
+hipError_t launch_tree_attention(const AttendParams &p, const TreeView &v, bool e4m3, void *ws,
+                                 hipStream_t s) {
+    if (!v.masks && v.sinks == 0) return launch_attention(p, e4m3, ws, s);
+    return launch_rows<true>(p, v, e4m3, s);
 }
 
 }  // namespace dspark

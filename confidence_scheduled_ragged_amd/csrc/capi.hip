@@ -456,11 +456,12 @@ PagedCache paged(const void *k_cache, const void *v_cache, int pages, int page_s
 
 }  // namespace
 
-DSPARK_API dspark_status dspark_append_kv(
+// depths: of the nodes of drafted trees, or NULL for chains.
+static dspark_status append_rows(
     const dspark_bf16 *q, const dspark_bf16 *k, const dspark_bf16 *v, long long q_stride,
     long long k_stride, long long v_stride, const float *cos, const float *sin, int positions,
-    int half, int interleaved, const int32_t *cu_seqlens, const int32_t *ctx_lens, int B, int rows,
-    int Hq, int Hkv, int D, void *k_cache, void *v_cache, int cache_type, int pages, int page_size,
+    int half, int interleaved, const int32_t *depths, const int32_t *cu_seqlens,
+    const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv, int D, void *k_cache, void *v_cache, int cache_type, int pages, int page_size,
     long long page_stride, long long head_stride, long long slot_stride, float k_scale,
     float v_scale, const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
     if (!q || !k || !v || !cu_seqlens || !ctx_lens || !k_cache || !v_cache || !block_table || !q_out)
@@ -474,7 +475,7 @@ DSPARK_API dspark_status dspark_append_kv(
     if (q_stride < 0 || k_stride < 0 || v_stride < 0) return DSPARK_ERR_ARG;
     if (misaligned(q, 2) || misaligned(k, 2) || misaligned(v, 2) || misaligned(q_out, 2) ||
         misaligned(cos, 4) || misaligned(sin, 4) || misaligned(cu_seqlens, 4) ||
-        misaligned(ctx_lens, 4) || misaligned(block_table, 4))
+        misaligned(ctx_lens, 4) || misaligned(block_table, 4) || misaligned(depths, 4))
         return DSPARK_ERR_ALIGN;
     AppendParams p;
     p.q = q;
@@ -498,7 +499,35 @@ DSPARK_API dspark_status dspark_append_kv(
     p.c = paged(k_cache, v_cache, pages, page_size, page_stride, head_stride, slot_stride, k_scale,
                 v_scale, e4m3, block_table, table_width);
     p.out = q_out;
+    p.depths = depths;
     return launched(launch_append_kv(p, interleaved != 0, e4m3, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_append_kv(
+    const dspark_bf16 *q, const dspark_bf16 *k, const dspark_bf16 *v, long long q_stride,
+    long long k_stride, long long v_stride, const float *cos, const float *sin, int positions,
+    int half, int interleaved, const int32_t *cu_seqlens, const int32_t *ctx_lens, int B, int rows,
+    int Hq, int Hkv, int D, void *k_cache, void *v_cache, int cache_type, int pages, int page_size,
+    long long page_stride, long long head_stride, long long slot_stride, float k_scale,
+    float v_scale, const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
+    return append_rows(q, k, v, q_stride, k_stride, v_stride, cos, sin, positions, half,
+                       interleaved, nullptr, cu_seqlens, ctx_lens, B, rows, Hq, Hkv, D, k_cache,
+                       v_cache, cache_type, pages, page_size, page_stride, head_stride,
+                       slot_stride, k_scale, v_scale, block_table, table_width, q_out, stream);
+}
+
+DSPARK_API dspark_status dspark_append_tree_kv(
+    const dspark_bf16 *q, const dspark_bf16 *k, const dspark_bf16 *v, long long q_stride,
+    long long k_stride, long long v_stride, const float *cos, const float *sin, int positions,
+    int half, int interleaved, const int32_t *depths, const int32_t *cu_seqlens,
+    const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv, int D, void *k_cache, void *v_cache, int cache_type, int pages, int page_size,
+    long long page_stride, long long head_stride, long long slot_stride, float k_scale,
+    float v_scale, const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
+    if (!depths) return DSPARK_ERR_NULL;
+    return append_rows(q, k, v, q_stride, k_stride, v_stride, cos, sin, positions, half,
+                       interleaved, depths, cu_seqlens, ctx_lens, B, rows, Hq, Hkv, D, k_cache,
+                       v_cache, cache_type, pages, page_size, page_stride, head_stride,
+                       slot_stride, k_scale, v_scale, block_table, table_width, q_out, stream);
 }
 
 DSPARK_API size_t dspark_attention_workspace_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
@@ -508,13 +537,14 @@ DSPARK_API size_t dspark_attention_workspace_bytes(int B, int max_rows, int Hq, 
     return attention_ws_bytes(B, max_rows, Hq, Hkv, D);
 }
 
-DSPARK_API dspark_status dspark_verify_attention(
+// The checks and parameters that both attention entry points share.
+static dspark_status attend_params(
     const dspark_bf16 *q, long long q_row, long long q_head, const void *k_cache,
     const void *v_cache, int cache_type, int pages, int page_size, long long page_stride,
     long long head_stride, long long slot_stride, float k_scale, float v_scale,
     const int32_t *block_table, int table_width, const int32_t *cu_seqlens,
     const int32_t *ctx_lens, int B, int rows, int max_rows, int Hq, int Hkv, int D, int window,
-    float scale, dspark_bf16 *out, void *ws, size_t ws_bytes, void *stream) {
+    float scale, dspark_bf16 *out, void *ws, size_t ws_bytes, AttendParams &p) {
     if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens || !ctx_lens || !out || !ws)
         return DSPARK_ERR_NULL;
     if (dspark_status st = check_paged(k_cache, v_cache, cache_type, pages, page_size, page_stride,
@@ -533,7 +563,6 @@ DSPARK_API dspark_status dspark_verify_attention(
     // a request has at most `rows` rows
     max_rows = max_rows < rows ? max_rows : rows;
     if (ws_bytes < attention_ws_bytes(B, max_rows, Hq, Hkv, D)) return DSPARK_ERR_WORKSPACE;
-    AttendParams p;
     p.q = q;
     p.q_row = q_row;
     p.q_head = q_head;
@@ -550,7 +579,52 @@ DSPARK_API dspark_status dspark_verify_attention(
     p.c = paged(k_cache, v_cache, pages, page_size, page_stride, head_stride, slot_stride, k_scale,
                 v_scale, e4m3, block_table, table_width);
     p.out = out;
-    return launched(launch_attention(p, e4m3, ws, as_stream(stream)));
+    return DSPARK_OK;
+}
+
+DSPARK_API dspark_status dspark_verify_attention(
+    const dspark_bf16 *q, long long q_row, long long q_head, const void *k_cache,
+    const void *v_cache, int cache_type, int pages, int page_size, long long page_stride,
+    long long head_stride, long long slot_stride, float k_scale, float v_scale,
+    const int32_t *block_table, int table_width, const int32_t *cu_seqlens,
+    const int32_t *ctx_lens, int B, int rows, int max_rows, int Hq, int Hkv, int D, int window,
+    float scale, dspark_bf16 *out, void *ws, size_t ws_bytes, void *stream) {
+    AttendParams p;
+    if (dspark_status st = attend_params(
+            q, q_row, q_head, k_cache, v_cache, cache_type, pages, page_size, page_stride,
+            head_stride, slot_stride, k_scale, v_scale, block_table, table_width, cu_seqlens,
+            ctx_lens, B, rows, max_rows, Hq, Hkv, D, window, scale, out, ws, ws_bytes, p))
+        return st;
+    return launched(launch_attention(p, cache_type == DSPARK_CACHE_E4M3, ws, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_tree_attention(
+    const dspark_bf16 *q, long long q_row, long long q_head, const void *k_cache,
+    const void *v_cache, int cache_type, int pages, int page_size, long long page_stride,
+    long long head_stride, long long slot_stride, float k_scale, float v_scale,
+    const int32_t *block_table, int table_width, const int32_t *cu_seqlens,
+    const int32_t *ctx_lens, int B, int rows, int max_rows, int Hq, int Hkv, int D, int window,
+    int sinks, const int32_t *depths, const int32_t *masks, int mask_words, float scale,
+    dspark_bf16 *out, void *ws, size_t ws_bytes, void *stream) {
+    if (!depths != !masks) return DSPARK_ERR_NULL;
+    AttendParams p;
+    if (dspark_status st = attend_params(
+            q, q_row, q_head, k_cache, v_cache, cache_type, pages, page_size, page_stride,
+            head_stride, slot_stride, k_scale, v_scale, block_table, table_width, cu_seqlens,
+            ctx_lens, B, rows, max_rows, Hq, Hkv, D, window, scale, out, ws, ws_bytes, p))
+        return st;
+    if (sinks < 0) return DSPARK_ERR_ARG;
+    if (masks && (mask_words < 1 || mask_words > DSPARK_MAX_ROWS / 32 ||
+                  (long long)mask_words * 32 < p.max_rows))
+        return DSPARK_ERR_SHAPE;
+    if (misaligned(depths, 4) || misaligned(masks, 4)) return DSPARK_ERR_ALIGN;
+    TreeView v;
+    v.depths = depths;
+    v.masks = reinterpret_cast<const uint32_t *>(masks);
+    v.words = masks ? mask_words : 0;
+    v.sinks = window > 0 ? sinks : 0;
+    return launched(launch_tree_attention(p, v, cache_type == DSPARK_CACHE_E4M3, ws,
+                                          as_stream(stream)));
 }
 
 DSPARK_API dspark_status dspark_sample_accept(
@@ -587,4 +661,209 @@ DSPARK_API dspark_status dspark_sample_accept(
     p.acc = accepted;
     p.bonus = bonus;
     return launched(launch_sample_accept(p, ws, as_stream(stream)));
+}
+
+namespace {
+
+// Requests, rows and tree sizes that the calls on drafted trees share.
+dspark_status check_tree(int B, int rows, int max_rows) {
+    if (B < 1 || B > DSPARK_MAX_ROWS || rows < 1 || rows > DSPARK_MAX_ROWS) return DSPARK_ERR_SHAPE;
+    if (max_rows < 1 || max_rows > DSPARK_MAX_TREE) return DSPARK_ERR_SHAPE;
+    return DSPARK_OK;
+}
+
+// The pools of all layers, as moves of whole rows see them.
+dspark_status page_moves(void *k_cache, void *v_cache, int cache_type, int layers,
+                         long long layer_stride, int pages, int page_size, long long page_stride,
+                         long long head_stride, long long slot_stride, int Hkv, int D,
+                         PageMoveParams &p) {
+    if (layers < 1 || layers > 32767 || pages < 1 || page_size < 1 || Hkv < 1 || Hkv > kMaxHeads ||
+        D < 1 || D > 1024)
+        return DSPARK_ERR_SHAPE;
+    if (cache_type != DSPARK_CACHE_BF16 && cache_type != DSPARK_CACHE_E4M3) return DSPARK_ERR_ARG;
+    if (layer_stride < 0 || page_stride < 0 || head_stride < 0 || slot_stride < 0)
+        return DSPARK_ERR_ARG;
+    const int item = cache_type == DSPARK_CACHE_E4M3 ? 1 : 2;
+    if (misaligned(k_cache, item) || misaligned(v_cache, item)) return DSPARK_ERR_ALIGN;
+    p.k = k_cache;
+    p.v = v_cache;
+    p.layers = layers;
+    p.pages = pages;
+    p.page = page_size;
+    p.heads = Hkv;
+    p.row_bytes = D * item;
+    p.layer_stride = layer_stride * item;
+    p.page_stride = page_stride * item;
+    p.head_stride = head_stride * item;
+    p.slot_stride = slot_stride * item;
+    return DSPARK_OK;
+}
+
+dspark_status check_pool(const int32_t *table, const int32_t *held, const int32_t *lens, int R,
+                         int width, int page_size, const int32_t *refs, int pages) {
+    if (!table || !held || !lens || !refs) return DSPARK_ERR_NULL;
+    if (R < 1 || R > DSPARK_MAX_TABLE_ROWS || width < 1 || page_size < 1 || pages < 1 ||
+        pages > (1 << 30) || (long long)width * page_size > 0x7FFFFFFFll ||
+        (long long)R * width > (1ll << 40))
+        return DSPARK_ERR_SHAPE;
+    if (misaligned(table, 4) || misaligned(held, 4) || misaligned(lens, 4) || misaligned(refs, 4))
+        return DSPARK_ERR_ALIGN;
+    return DSPARK_OK;
+}
+
+PoolParams pool_params(int32_t *table, int32_t *held, const int32_t *lens, int R, int width,
+                       int page_size, int32_t *refs, int pages) {
+    PoolParams p = {};
+    p.table = table;
+    p.held = held;
+    p.lens = lens;
+    p.R = R;
+    p.width = width;
+    p.page = page_size;
+    p.refs = refs;
+    p.pages = pages;
+    return p;
+}
+
+}  // namespace
+
+DSPARK_API dspark_status dspark_tree_masks(const int32_t *parents, const int32_t *cu_seqlens,
+                                           const int32_t *ctx_lens, int B, int rows, int max_rows,
+                                           int window, int sinks, int mask_words, int32_t *depths,
+                                           int32_t *masks, void *stream) {
+    if (!parents || !cu_seqlens || !depths || !masks) return DSPARK_ERR_NULL;
+    if (dspark_status st = check_tree(B, rows, max_rows)) return st;
+    max_rows = max_rows < rows ? max_rows : rows;
+    if (mask_words < 1 || mask_words > DSPARK_MAX_TREE / 32 || mask_words * 32 < max_rows)
+        return DSPARK_ERR_SHAPE;
+    if (window < 0 || sinks < 0) return DSPARK_ERR_ARG;
+    if (window > 0 && sinks > 0 && !ctx_lens) return DSPARK_ERR_NULL;
+    if (misaligned(parents, 4) || misaligned(cu_seqlens, 4) || misaligned(ctx_lens, 4) ||
+        misaligned(depths, 4) || misaligned(masks, 4))
+        return DSPARK_ERR_ALIGN;
+    TreeMaskParams p;
+    p.parents = parents;
+    p.cu = cu_seqlens;
+    p.ctx = ctx_lens;
+    p.B = B;
+    p.rows = rows;
+    p.max_rows = max_rows;
+    p.words = mask_words;
+    p.window = window;
+    p.sinks = window > 0 ? sinks : 0;
+    p.depths = depths;
+    p.masks = reinterpret_cast<uint32_t *>(masks);
+    return launched(launch_tree_masks(p, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_tree_accept(const int32_t *packed_choice,
+                                            const int32_t *packed_tokens, const int32_t *parents,
+                                            const int32_t *cu_seqlens, int B, int rows,
+                                            int max_rows, int width, int32_t *accepted,
+                                            int32_t *bonus, int32_t *path, void *stream) {
+    if (!packed_choice || !packed_tokens || !parents || !cu_seqlens || !accepted || !bonus || !path)
+        return DSPARK_ERR_NULL;
+    if (dspark_status st = check_tree(B, rows, max_rows)) return st;
+    if (width < 1 || width > DSPARK_MAX_TREE) return DSPARK_ERR_SHAPE;
+    if (misaligned(packed_choice, 4) || misaligned(packed_tokens, 4) || misaligned(parents, 4) ||
+        misaligned(cu_seqlens, 4) || misaligned(accepted, 4) || misaligned(bonus, 4) ||
+        misaligned(path, 4))
+        return DSPARK_ERR_ALIGN;
+    TreeAcceptParams p;
+    p.choice = packed_choice;
+    p.tokens = packed_tokens;
+    p.parents = parents;
+    p.cu = cu_seqlens;
+    p.B = B;
+    p.rows = rows;
+    p.max_rows = max_rows;
+    p.width = width;
+    p.accepted = accepted;
+    p.bonus = bonus;
+    p.path = path;
+    return launched(launch_tree_accept(p, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_move_kv(void *k_cache, void *v_cache, int cache_type, int layers,
+                                        long long layer_stride, int pages, int page_size,
+                                        long long page_stride, long long head_stride,
+                                        long long slot_stride, int Hkv, int D, const int32_t *path,
+                                        const int32_t *accepted, int width,
+                                        const int32_t *ctx_lens, const int32_t *block_table,
+                                        int table_width, int B, void *stream) {
+    if (!k_cache || !v_cache || !path || !accepted || !ctx_lens || !block_table)
+        return DSPARK_ERR_NULL;
+    if (B < 1 || B > DSPARK_MAX_ROWS || width < 1 || width > DSPARK_MAX_TREE || table_width < 1 ||
+        page_size < 1 || (long long)table_width * page_size > 0x7FFFFFFFll)
+        return DSPARK_ERR_SHAPE;
+    PageMoveParams p = {};
+    if (dspark_status st = page_moves(k_cache, v_cache, cache_type, layers, layer_stride, pages,
+                                      page_size, page_stride, head_stride, slot_stride, Hkv, D, p))
+        return st;
+    if (misaligned(path, 4) || misaligned(accepted, 4) || misaligned(ctx_lens, 4) ||
+        misaligned(block_table, 4))
+        return DSPARK_ERR_ALIGN;
+    p.c = paged(k_cache, v_cache, pages, page_size, p.page_stride, p.head_stride, p.slot_stride,
+                1.f, 1.f, false, block_table, table_width);
+    p.path = path;
+    p.accepted = accepted;
+    p.width = width;
+    p.ctx = ctx_lens;
+    p.n = B;
+    return launched(launch_move_kv(p, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_copy_pages(void *k_cache, void *v_cache, int cache_type,
+                                           int layers, long long layer_stride, int pages,
+                                           int page_size, long long page_stride,
+                                           long long head_stride, long long slot_stride, int Hkv,
+                                           int D, const int32_t *src, const int32_t *dst,
+                                           const int32_t *slots, int n, void *stream) {
+    if (!k_cache || !v_cache || !src || !dst) return DSPARK_ERR_NULL;
+    if (n < 1 || n > (1 << 20)) return DSPARK_ERR_SHAPE;
+    PageMoveParams p = {};
+    if (dspark_status st = page_moves(k_cache, v_cache, cache_type, layers, layer_stride, pages,
+                                      page_size, page_stride, head_stride, slot_stride, Hkv, D, p))
+        return st;
+    if (misaligned(src, 4) || misaligned(dst, 4) || misaligned(slots, 4)) return DSPARK_ERR_ALIGN;
+    p.src = src;
+    p.dst = dst;
+    p.slots = slots;
+    p.n = n;
+    return launched(launch_copy_pages(p, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_resize_pages(int32_t *table, int32_t *held, const int32_t *lens,
+                                             int R, int width, int page_size, int32_t *refs,
+                                             int pages, int32_t *granted, void *stream) {
+    if (!granted) return DSPARK_ERR_NULL;
+    if (dspark_status st = check_pool(table, held, lens, R, width, page_size, refs, pages))
+        return st;
+    if (misaligned(granted, 4)) return DSPARK_ERR_ALIGN;
+    PoolParams p = pool_params(table, held, lens, R, width, page_size, refs, pages);
+    p.granted = granted;
+    return launched(launch_resize_pages(p, as_stream(stream)));
+}
+
+DSPARK_API dspark_status dspark_fork_pages(int32_t *table, int32_t *held, const int32_t *lens,
+                                           int R, int width, int page_size, int32_t *refs,
+                                           int pages, const int32_t *src, const int32_t *dst,
+                                           int n, int32_t *copy_src, int32_t *copy_dst,
+                                           int32_t *copy_slots, int32_t *granted, void *stream) {
+    if (!src || !dst || !copy_src || !copy_dst || !copy_slots || !granted) return DSPARK_ERR_NULL;
+    if (dspark_status st = check_pool(table, held, lens, R, width, page_size, refs, pages))
+        return st;
+    if (n < 1 || n > DSPARK_MAX_FORKS) return DSPARK_ERR_SHAPE;
+    if (misaligned(src, 4) || misaligned(dst, 4) || misaligned(copy_src, 4) ||
+        misaligned(copy_dst, 4) || misaligned(copy_slots, 4) || misaligned(granted, 4))
+        return DSPARK_ERR_ALIGN;
+    PoolParams p = pool_params(table, held, lens, R, width, page_size, refs, pages);
+    p.src = src;
+    p.dst = dst;
+    p.n = n;
+    p.copy_src = copy_src;
+    p.copy_dst = copy_dst;
+    p.copy_slots = copy_slots;
+    p.granted = granted;
+    return launched(launch_fork_pages(p, as_stream(stream)));
 }

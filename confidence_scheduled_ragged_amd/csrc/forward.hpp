@@ -102,7 +102,15 @@ struct AppendParams {
     int B, rows, Hq, Hkv, D;
     PagedCache c;
     uint16_t *out;  // [rows, Hq, D]
+    const int32_t *depths;  // [rows], drafted trees only
 };
+
+// Steps from a root that row j of a request stands at: never more than there are rows
+// before it.
+__device__ __forceinline__ int depth_of(const int32_t *depths, int64_t r, int j) {
+    const int d = depths[r];
+    return d < 0 ? 0 : (d > j ? j : d);
+}
 
 hipError_t launch_append_kv(const AppendParams &p, bool interleaved, bool e4m3, hipStream_t s);
 
@@ -116,9 +124,61 @@ struct AttendParams {
     uint16_t *out;  // [rows, Hq, D]
 };
 
+// What dspark_tree_attention adds: rows that see some of their request's rows
+// (masks and depths, or none for a chain) and first positions that stay visible.
+struct TreeView {
+    const int32_t *depths;   // [rows]
+    const uint32_t *masks;   // [rows, words]
+    int words, sinks;
+};
+
 // Scratch of the attention kernels for valid sizes.
 size_t attention_ws_bytes(int B, int max_rows, int Hq, int Hkv, int D);
 hipError_t launch_attention(const AttendParams &p, bool e4m3, void *ws, hipStream_t s);
+hipError_t launch_tree_attention(const AttendParams &p, const TreeView &v, bool e4m3, void *ws,
+                                 hipStream_t s);
+
+struct TreeMaskParams {
+    const int32_t *parents, *cu, *ctx;  // ctx nullable
+    int B, rows, max_rows, words, window, sinks;
+    int32_t *depths;
+    uint32_t *masks;
+};
+hipError_t launch_tree_masks(const TreeMaskParams &p, hipStream_t s);
+
+struct TreeAcceptParams {
+    const int32_t *choice, *tokens, *parents, *cu;
+    int B, rows, max_rows, width;
+    int32_t *accepted, *bonus, *path;
+};
+hipError_t launch_tree_accept(const TreeAcceptParams &p, hipStream_t s);
+
+// Rows of a block table over a pool of pages; forks of some of them.
+struct PoolParams {
+    int32_t *table, *held, *refs;
+    const int32_t *lens;
+    int R, width, page, pages;
+    const int32_t *src, *dst;
+    int n;
+    int32_t *copy_src, *copy_dst, *copy_slots, *granted;
+};
+hipError_t launch_resize_pages(const PoolParams &p, hipStream_t s);
+hipError_t launch_fork_pages(const PoolParams &p, hipStream_t s);
+
+// Moves of whole rows of D values in the pools of all layers; strides in bytes, also
+// those of `c`, whose table the moves of a path use.
+struct PageMoveParams {
+    void *k, *v;
+    int layers, pages, page, heads, row_bytes;
+    int64_t layer_stride, page_stride, head_stride, slot_stride;
+    int n;  // copies, or requests
+    const int32_t *src, *dst, *slots;
+    PagedCache c;
+    const int32_t *path, *accepted, *ctx;
+    int width;
+};
+hipError_t launch_copy_pages(const PageMoveParams &p, hipStream_t s);
+hipError_t launch_move_kv(const PageMoveParams &p, hipStream_t s);
 
 struct SampleParams {
     const uint16_t *logits;

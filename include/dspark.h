@@ -493,6 +493,197 @@ dspark_status dspark_sample_accept(const dspark_bf16 *logits, const int32_t *pac
                                    int32_t *accepted, int32_t *bonus, void *ws, size_t ws_bytes,
                                    void *stream);
 
+/* ------------------------------------------- drafted trees and shared pages
+ *
+ * A request may draft a tree instead of a chain: its packed rows are the tree's
+ * nodes, row 0 the last committed token, and parents[r] the place among the
+ * request's rows of row r's parent, which lies below row r's own place (any other
+ * value makes the row a root). A node has the slot of its row, ctx_lens[b] + j, as
+ * in a chain, and the position ctx_lens[b] + depth, depth being the steps to its
+ * root. A step over trees: dspark_tree_masks once, per layer dspark_append_tree_kv
+ * and dspark_tree_attention, then the target's choices (packed_argmax of
+ * dspark_accept or packed_sample of dspark_sample_accept), dspark_tree_accept, and
+ * dspark_move_kv, which brings the accepted nodes' keys and values together.
+ */
+#define DSPARK_MAX_TREE 1024        /* nodes of a request's tree */
+#define DSPARK_MAX_TABLE_ROWS (1 << 20)
+#define DSPARK_MAX_FORKS 16384
+
+/*
+ * The depth of every node and the rows of its request that it sees, itself and its
+ * ancestors, as bits: bit i % 32 of word i / 32 of masks[r] is 1 when row r sees
+ * row i of its request. With window > 0 an ancestor is seen when it is fewer than
+ * `window` levels up, or its position is below `sinks`, so that layers with
+ * another window or other sinks take masks of their own (or the same, where no
+ * tree is as deep as the window).
+ * parents [rows], cu_seqlens [B+1] int32; ctx_lens [B] int32, read where window
+ * and sinks are above 0 and NULL otherwise if wanted; depths [rows], masks [rows,
+ * mask_words] int32 outputs. Rows at and past cu_seqlens[B], and a request's rows
+ * past max_rows, are untouched.
+ * DSPARK_ERR_SHAPE: B, rows or max_rows below 1, rows or B above DSPARK_MAX_ROWS,
+ * max_rows above DSPARK_MAX_TREE, mask_words * 32 below the smaller of max_rows and
+ * rows or above DSPARK_MAX_TREE; DSPARK_ERR_ARG: a negative window or sinks.
+ */
+dspark_status dspark_tree_masks(const int32_t *parents, const int32_t *cu_seqlens,
+                                const int32_t *ctx_lens, int B, int rows, int max_rows,
+                                int window, int sinks, int mask_words, int32_t *depths,
+                                int32_t *masks, void *stream);
+
+/*
+ * dspark_append_kv for the nodes of trees: row j of request b is rotated by the
+ * angles of position ctx_lens[b] + depths[r] and written to slot ctx_lens[b] + j.
+ * depths [rows] int32, of which what lies outside [0, j] counts as the nearest of
+ * these. Rows whose position is not below `positions` are untouched. Other
+ * arguments, results and checks are dspark_append_kv's.
+ */
+dspark_status dspark_append_tree_kv(const dspark_bf16 *q, const dspark_bf16 *k,
+                                    const dspark_bf16 *v, long long q_stride, long long k_stride,
+                                    long long v_stride, const float *cos, const float *sin,
+                                    int positions, int half, int interleaved,
+                                    const int32_t *depths, const int32_t *cu_seqlens,
+                                    const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv,
+                                    int D, void *k_cache, void *v_cache, int cache_type, int pages,
+                                    int page_size, long long page_stride, long long head_stride,
+                                    long long slot_stride, float k_scale, float v_scale,
+                                    const int32_t *block_table, int table_width,
+                                    dspark_bf16 *q_out, void *stream);
+
+/*
+ * dspark_verify_attention for the nodes of trees, and with first positions that a
+ * window leaves visible. With p the position of a row (ctx_lens[b] + depths[r],
+ * depths taken as in dspark_append_tree_kv), it sees
+ *   the context's positions t < ctx_lens[b] with t > p - window or t < sinks (all
+ *     when window is 0; sinks then has no effect);
+ *   of its request's rows, which stand in slots from ctx_lens[b] on, those whose
+ *     bit is set in masks[r], whatever the window (dspark_tree_masks keeps to it);
+ *     bits of rows past the request's own, or past max_rows, have no effect. Any
+ *     bits are served, those of later rows too.
+ * With depths and masks NULL the rows are a chain, as for dspark_verify_attention:
+ * p = ctx_lens[b] + j, and a row sees the positions t <= p with t > p - window or
+ * t < sinks.
+ * Positions whose page the table does not name are not seen. depths [rows], masks
+ * [rows, mask_words] int32: both or neither (DSPARK_ERR_NULL); DSPARK_ERR_SHAPE for
+ * mask_words * 32 below the smaller of max_rows and rows; DSPARK_ERR_ARG for
+ * negative sinks. Everything else, the weights' rounding, rows that see nothing,
+ * values that are not finite, the alignment and the workspace, is as for
+ * dspark_verify_attention, whose workspace serves both.
+ */
+dspark_status dspark_tree_attention(const dspark_bf16 *q, long long q_row, long long q_head,
+                                    const void *k_cache, const void *v_cache, int cache_type,
+                                    int pages, int page_size, long long page_stride,
+                                    long long head_stride, long long slot_stride, float k_scale,
+                                    float v_scale, const int32_t *block_table, int table_width,
+                                    const int32_t *cu_seqlens, const int32_t *ctx_lens, int B,
+                                    int rows, int max_rows, int Hq, int Hkv, int D, int window,
+                                    int sinks, const int32_t *depths, const int32_t *masks,
+                                    int mask_words, float scale, dspark_bf16 *out, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/*
+ * The longest way down a tree that the target agrees with. From row 0 of request
+ * b on, the next row is the lowest one that has the current row for its parent and
+ * the target's choice at the current row for its token:
+ *   path[b, 0] = 0, path[b, i+1] = min{c : parents[c] = path[b, i],
+ *                                      packed_tokens[c] = packed_choice[path[b, i]]}
+ *   accepted[b] = the number of steps, at most width - 1
+ *   bonus[b]    = packed_choice[path[b, accepted[b]]]
+ * (places among the request's rows). Entries of path past accepted[b] are -1; a
+ * request without rows gets accepted 0, bonus -1 and a path of -1. On a chain this
+ * is dspark_accept's result.
+ * packed_choice, packed_tokens, parents [rows], cu_seqlens [B+1] int32; rows of a
+ * request past max_rows are left out; accepted, bonus [B], path [B, width] int32
+ * outputs. DSPARK_ERR_SHAPE as for dspark_tree_masks, and for a width below 1 or
+ * above DSPARK_MAX_TREE.
+ */
+dspark_status dspark_tree_accept(const int32_t *packed_choice, const int32_t *packed_tokens,
+                                 const int32_t *parents, const int32_t *cu_seqlens, int B,
+                                 int rows, int max_rows, int width, int32_t *accepted,
+                                 int32_t *bonus, int32_t *path, void *stream);
+
+/*
+ * Brings an accepted path together in the paged cache of all layers: for every
+ * request, the keys and values in slot ctx_lens[b] + path[b, i] go to slot
+ * ctx_lens[b] + i, for i = 1 .. min(accepted[b], width - 1). The cache then holds
+ * the committed tokens in a row, at the positions that they were rotated by.
+ * k_cache, v_cache: layer l lies l * layer_stride elements behind the first; other
+ * strides and the table as for dspark_append_kv. path [B, width] rises in every row
+ * with path[b, i] >= i, as dspark_tree_accept leaves it (where it does not, what
+ * the slots hold afterwards is unspecified, and nothing else is touched); a
+ * negative entry, or a slot without a page, moves nothing. Pages that requests
+ * share must not be written by the call. accepted, ctx_lens [B], block_table [B,
+ * table_width] int32.
+ * DSPARK_ERR_SHAPE: layers, pages, page_size, Hkv, D, width, table_width or B below
+ * 1, layers above 32767, Hkv above 4096, D above 1024, width above DSPARK_MAX_TREE,
+ * B above DSPARK_MAX_ROWS; DSPARK_ERR_ARG: an unknown cache_type, a negative stride.
+ */
+dspark_status dspark_move_kv(void *k_cache, void *v_cache, int cache_type, int layers,
+                             long long layer_stride, int pages, int page_size,
+                             long long page_stride, long long head_stride, long long slot_stride,
+                             int Hkv, int D, const int32_t *path, const int32_t *accepted,
+                             int width, const int32_t *ctx_lens, const int32_t *block_table,
+                             int table_width, int B, void *stream);
+
+/*
+ * Pages of the cache on the device. A pool's state: refs [pages], how many table
+ * entries name a page (0: it is free), a table [R, width], and held [R], how many
+ * pages a row holds, named by its first entries; other entries are -1 where these
+ * calls have written them. A new pool has refs and held 0 and the table -1. The
+ * calls read and write this state, in the order of their stream; several tables may
+ * share refs.
+ *
+ * dspark_resize_pages: row b holds ceil(lens[b] / page_size) pages afterwards. First
+ * every row's pages past its length are released, then the rows that hold too few
+ * get free pages, the lowest first, in the order of the rows. The first row that
+ * cannot have all that it needs and the rows behind it get none. A row whose length
+ * needs more than `width` pages is left as it is. granted[b] is 1 where row b holds
+ * what its length needs. Negative lengths count as 0.
+ *   Called with ctx_lens plus a step's rows before the step, and with 0 for a
+ * request that ends, it is all the page keeping of a serving loop. A page that
+ * several rows share is for reading: a row cut back into one needs dspark_fork_pages
+ * before more is appended to it.
+ * table, held, refs int32 in and out; lens [R] int32; granted [R] int32 output.
+ * DSPARK_ERR_SHAPE: R, width, page_size or pages below 1, R above
+ * DSPARK_MAX_TABLE_ROWS, pages above 2^30, width * page_size above 2^31 - 1.
+ */
+dspark_status dspark_resize_pages(int32_t *table, int32_t *held, const int32_t *lens, int R,
+                                  int width, int page_size, int32_t *refs, int pages,
+                                  int32_t *granted, void *stream);
+
+/*
+ * Continuations that share pages: for i in [0, n), row dst[i] releases what it held
+ * and becomes a copy of row src[i] up to position lens[src[i]] (at most what that row
+ * holds). Pages that these positions fill are shared; where they end inside a page,
+ * dst[i] gets a free page of its own, the lowest first in the order of i, and
+ * (copy_src[i], copy_dst[i], copy_slots[i]) says which page has to be copied to which
+ * and how many slots of it, as dspark_copy_pages takes them (-1, -1, 0 where nothing
+ * has to be). granted[i] is 1 where this was done. It is 0, and row dst[i] as it was,
+ * where a row number lies outside [0, R), where dst[i] is the target of an earlier
+ * entry or the source of any, and where a free page is needed and there is none left
+ * (pages that the call itself releases are free for later calls).
+ * src, dst, copy_src, copy_dst, copy_slots, granted [n] int32. Other arguments and
+ * checks as for dspark_resize_pages, and DSPARK_ERR_SHAPE for n below 1 or above
+ * DSPARK_MAX_FORKS.
+ */
+dspark_status dspark_fork_pages(int32_t *table, int32_t *held, const int32_t *lens, int R,
+                                int width, int page_size, int32_t *refs, int pages,
+                                const int32_t *src, const int32_t *dst, int n, int32_t *copy_src,
+                                int32_t *copy_dst, int32_t *copy_slots, int32_t *granted,
+                                void *stream);
+
+/*
+ * Copies pages of the cache in all layers, keys and values: the first slots[i] slots
+ * (all where slots is NULL; counts outside [0, page_size] are the nearest of these)
+ * of page src[i] to page dst[i], for i in [0, n). Where src[i] or dst[i] lies outside
+ * [0, pages), or they are the same, nothing is copied. No page may be written by one
+ * copy of a call and read or written by another one. Pools as for dspark_move_kv.
+ * DSPARK_ERR_SHAPE as there, and for n below 1 or above 2^20.
+ */
+dspark_status dspark_copy_pages(void *k_cache, void *v_cache, int cache_type, int layers,
+                                long long layer_stride, int pages, int page_size,
+                                long long page_stride, long long head_stride,
+                                long long slot_stride, int Hkv, int D, const int32_t *src,
+                                const int32_t *dst, const int32_t *slots, int n, void *stream);
+
 /* Scratch bytes needed by dspark_accept and dspark_step for these sizes
  * (independent of d); 0 for invalid sizes. */
 size_t dspark_workspace_bytes(int B, int gamma, int V);
