@@ -4,7 +4,9 @@ Every .hip source under csrc/ is compiled to an object in _build/ (in
 parallel), then linked into confidence_scheduled_ragged_amd/libdspark.so.
 The fused step (fused.hip) is compiled twice: once as is, once with
 DSPARK_SLOTS32=1 (its kernels without 64-bit division, for steps whose slot
-counts fit in 32 bits). Packed-fp32 instructions are disabled for device code.
+counts fit in 32 bits), and so is the attention (attend.hip), once for chains and
+once with DSPARK_TREE=1 for drafted trees. Packed-fp32 instructions are disabled for
+device code.
 """
 import glob
 import os
@@ -34,6 +36,7 @@ def units():
     """(source, extra flags, object name) of every object in the library."""
     out = [(src, [], os.path.basename(src) + ".o") for src in sources()]
     out.append((os.path.join(CSRC, "fused.hip"), ["-DDSPARK_SLOTS32=1"], "fused_slots32.o"))
+    out.append((os.path.join(CSRC, "attend.hip"), ["-DDSPARK_TREE=1"], "attend_trees.o"))
     return out
 
 

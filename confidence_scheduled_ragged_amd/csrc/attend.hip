@@ -7,11 +7,26 @@
 //   O = sum_t exp(x_t - m) V_t / sum_t exp(x_t - m),  x_t = scale (q . K_t),
 // with m the largest x_t. A running maximum and sum carry the softmax over the
 // keys in one pass; a row that sees nothing gives zeros.
+//
+// Compiled twice: as is, for rows in a chain, and with DSPARK_TREE=1 for the nodes of
+// drafted trees and for windows with first positions that stay visible (the rows that
+// TreeView describes). One kernel for both would cost the chains registers.
 #include <type_traits>
 
 #include "forward.hpp"
 
+#ifndef DSPARK_TREE
+#define DSPARK_TREE 0
+#endif
+
 namespace dspark {
+#if DSPARK_TREE
+namespace trees {
+#else
+namespace chains {
+#endif
+
+constexpr bool kTree = DSPARK_TREE;
 
 constexpr int kMaxHeadDim = 256;
 constexpr int kRowThreads = 64;
@@ -56,8 +71,8 @@ __device__ __forceinline__ float load1(const void *pool, int64_t at) {
 // time, a lane per key for the scores and a lane per output element for the
 // weighted values. Bound by its latency: 32 requests of mixed traffic at D = 96 took
 // 2127 us here and take 66 us in the tiles below, so only heads over 128 and pools
-// that 16-byte loads do not fit come here. kTree: the rows that TreeView describes.
-template <bool kE4m3, bool kTree>
+// that 16-byte loads do not fit come here.
+template <bool kE4m3>
 __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p, TreeView v) {
     __shared__ float q_s[kMaxHeadDim];
     __shared__ float p_s[kWave];
@@ -208,6 +223,9 @@ struct TileParams {
     // 16 slots in a row share a page, and a page and 16 slots are below 2^32 bytes
     bool together;
     uint32_t page_bytes, slot_bytes;
+#if DSPARK_TREE
+    TreeView v;
+#endif
 };
 
 // The call's parameters, read again from the kernel's arguments: for what runs once
@@ -261,12 +279,33 @@ __device__ __forceinline__ Request scalar_request(const AttendParams &p, int b) 
 }
 // Positions [lo, hi) that block i of a request needs, its first and last row's
 // positions, and its tiles (one at least: a block that sees nothing still writes
-// its zeros).
+// its zeros). Rows with masks may see any row of their request, so that only the
+// context is common to all; their positions are at most the last row's. `sink` tiles
+// from the first on stay visible below the window's.
 struct Block {
     int lo, hi, first, final, tile, tiles;
+#if DSPARK_TREE
+    int sink;
+#endif
+    // the i-th tile
+    __device__ __forceinline__ int at(int i) const {
+#if DSPARK_TREE
+        return i < sink ? i : tile + i - sink;
+#else
+        return tile + i;
+#endif
+    }
+    __device__ __forceinline__ int after(int t) const {  // the tile after tile t
+#if DSPARK_TREE
+        return t + 1 == sink && t + 1 < tile ? tile : t + 1;
+#else
+        return t + 1;
+#endif
+    }
 };
 template <int kBlockRows, int kKeys>
-__device__ __forceinline__ Block block_of(const AttendParams &p, const Request &q, int i) {
+__device__ __forceinline__ Block block_of(const TileParams &tp, const Request &q, int i) {
+    const AttendParams &p = tp.a;
     const int G = p.Hq / p.Hkv;
     const int m0 = i * kBlockRows;
     const int m1 = (q.M < m0 + kBlockRows ? q.M : m0 + kBlockRows) - 1;
@@ -274,13 +313,27 @@ __device__ __forceinline__ Block block_of(const AttendParams &p, const Request &
     Block k;
     k.first = q.ctx + m0 / G;
     k.final = q.ctx + m1 / G;
+#if DSPARK_TREE
+    if (tp.v.masks) {
+        k.first = q.ctx;
+        k.final = q.ctx + q.M / G - 1;
+    }
+#endif
     k.lo = 0;
     if (p.window > 0 && k.first + 1 > p.window) k.lo = k.first + 1 - p.window;
     const int end = k.final + 1;
     k.hi = end < width ? end : (int)width;
     k.tile = k.lo / kKeys;
     const int last = (int)(((int64_t)k.hi + kKeys - 1) / kKeys);
-    k.tiles = last > k.tile ? last - k.tile : 1;
+    k.tiles = last > k.tile ? last - k.tile : 0;
+#if DSPARK_TREE
+    if (tp.v.masks) k.first = q.ctx - 1;
+    const int sinks = tp.v.sinks < k.hi ? tp.v.sinks : k.hi;
+    const int sink = (sinks + kKeys - 1) / kKeys;
+    k.sink = sink < k.tile ? sink : k.tile;
+    k.tiles += k.sink;
+#endif
+    if (k.tiles == 0) k.tiles = 1;
     return k;
 }
 
@@ -368,6 +421,9 @@ struct Tiles {
         f32x2 ml[kWaves / 2 * kWave];
         // rows whose values were not all finite, per staging wave
         uint64_t bad[kSlots][kStagers * kRowWords];
+#if DSPARK_TREE
+        uint64_t bits[kThreads];  // of each lane's row, where 64 are enough
+#endif
         int last;
     };
 
@@ -414,6 +470,11 @@ struct Tiles {
         int pos_min, pos_max;  // over the wave's query rows
         bool active, hole;     // hole: some position may have no page
         float c;               // scores to powers of two
+#if DSPARK_TREE
+        int border;            // positions from here on are seen by the row's bits
+        int sinks;
+        const uint32_t *mask;  // of the row, where it has more than 64 bits
+#endif
     };
     struct State {
         bf16x8 q[D / 16];
@@ -529,6 +590,9 @@ struct Tiles {
     // the rows that see them.
     __device__ static __forceinline__ bool partial(const AttendParams &p, const Task &t, int tile) {
         const int k0 = tile * kKeys;
+#if DSPARK_TREE
+        if (k0 + kKeys <= t.sinks) return k0 + kKeys - 1 > t.first;
+#endif
         return k0 + kKeys - 1 > t.first || (p.window > 0 && k0 <= t.final - p.window);
     }
     __device__ static __forceinline__ bool bad_word(uint32_t x) {
@@ -587,9 +651,10 @@ struct Tiles {
     // any.
     __device__ static __forceinline__ void add_bad(const uint64_t *bad, int tile, int sub,
                                                    const AttendParams &p, const Task &t,
-                                                   State &st, int lane) {
+                                                   State &st, const Lds &s, int lane) {
         const int h = lane >> 5;
         const AttendParams cold = params_again().a;
+        const uint32_t bits = bits_of(s, t, tile * kKeys + sub * 32);
 #pragma unroll 1
         for (int y = sub * 32; y < sub * 32 + 32; ++y) {
             if (!(bad[y / kWaveRows * kRowWords + y % kWaveRows / 64] >> (y % kWaveRows % 64) & 1))
@@ -597,7 +662,7 @@ struct Tiles {
             const int key = tile * kKeys + y;
             const int64_t at = slot_offset(cold.c, t.table, key, 0);
             if (at < 0) continue;
-            const bool see = visible(p, t, key);
+            const bool see = visible(p, t, key, bits >> (y & 31) & 1);
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -612,10 +677,35 @@ struct Tiles {
     }
 
     // ------------------------------------------------------------- compute
-    // Whether this lane's query row sees a position that has a page.
-    __device__ static __forceinline__ bool visible(const AttendParams &p, const Task &t, int key) {
+    // Whether this lane's query row sees a position that has a page; `bit`: of its mask.
+    __device__ static __forceinline__ bool visible(const AttendParams &p, const Task &t, int key,
+                                                   bool bit) {
+#if DSPARK_TREE
+        const bool near = p.window == 0 || key > t.pos - p.window || key < t.sinks;
+        return key < t.hi && (key < t.border ? key <= t.pos && near : bit);
+#else
         return key <= t.pos && key >= t.lo && key < t.hi &&
                (p.window == 0 || key > t.pos - p.window);
+#endif
+    }
+    // The bits of this lane's row for 32 positions from k0 on, 0 below the border. Kept in
+    // LDS: a load from memory would wait for the tiles on their way.
+    __device__ static __forceinline__ uint32_t bits_of(const Lds &s, const Task &t, int k0) {
+#if DSPARK_TREE
+        const int64_t base = (int64_t)k0 - t.border;
+        if (base <= -32) return 0;
+        const int words = params_again().v.words;
+        if (words <= 2) {
+            const uint64_t m = s.bits[threadIdx.x];
+            return base >= 64 ? 0u : (uint32_t)(base < 0 ? m << -base : m >> base);
+        }
+        const int w = (int)(base >> 5);
+        const uint64_t lo = w >= 0 && w < words ? t.mask[w] : 0u;
+        const uint64_t hi = w + 1 < words ? t.mask[w + 1] : 0u;
+        return (uint32_t)((lo | hi << 32) >> (base & 31));
+#else
+        return 0;
+#endif
     }
     __device__ static __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
         const u32x4 x = {
@@ -760,14 +850,22 @@ struct Tiles {
     template <int kSub>
     __device__ static __forceinline__ void compute(const Slots &slots, int number, int tile, int sub,
                                                    const AttendParams &p, const Task &t,
-                                                   State &st, int lane) {
+                                                   State &st, const Lds &s, int lane) {
         const int h = lane >> 5;
         const int k0 = tile * kKeys + sub * 32, k1 = k0 + kSub * 32 - 1;
+#if DSPARK_TREE
+        if (k0 > t.pos_max || k0 >= t.hi ||
+            (k0 >= t.sinks && p.window > 0 && k1 <= t.pos_min - p.window))
+            return;
+        const bool whole = k1 <= t.pos_min && k1 < t.hi && !t.hole &&
+                           (p.window == 0 || k0 > t.pos_max - p.window || k1 < t.sinks);
+#else
         if (k0 > t.pos_max || k0 >= t.hi || k1 < t.lo ||
             (p.window > 0 && k1 <= t.pos_min - p.window))
             return;
         const bool whole = k1 <= t.pos_min && k1 < t.hi && k0 >= t.lo && !t.hole &&
                            (p.window == 0 || k0 > t.pos_max - p.window);
+#endif
         // scores, transposed: keys down the registers, queries across the lanes
         f32x16 x[kSub];
 #pragma unroll
@@ -801,11 +899,13 @@ struct Tiles {
                 if (t.hole)
                     no = (uint32_t)__ballot(slot_offset(params_again().a.c, t.table,
                                                         k0 + i * 32 + (lane & 31), 0) < 0);
+                const uint32_t bits = bits_of(s, t, k0 + i * 32);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int y = 8 * (r / 4) + 4 * h + (r & 3);
-                    x[i][r] = visible(p, t, k0 + i * 32 + y) && !(no >> y & 1) ? x[i][r]
-                                                                               : -INFINITY;
+                    x[i][r] = visible(p, t, k0 + i * 32 + y, bits >> y & 1) && !(no >> y & 1)
+                                  ? x[i][r]
+                                  : -INFINITY;
                 }
             }
         }
@@ -891,7 +991,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     if ((int64_t)p.max_rows * G <= kBlockRows) {
         for (int b = tid; b < p.B; b += kTileThreads) {
             const Request q = load_request<kBlockRows>(p, b);
-            const int tiles = block_of<kBlockRows, T::kKeys>(p, q, 0).tiles;
+            const int tiles = block_of<kBlockRows, T::kKeys>(tp, q, 0).tiles;
             s.before[b + 1] = q.M > 0 ? (uint64_t)(kUnitTiles + tiles) * p.Hkv : 0;
         }
     } else {
@@ -899,7 +999,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
             const Request q = load_request<kBlockRows>(p, b);
             uint64_t n = 0;
             for (int i = lane; i < q.blocks; i += kWave)
-                n += kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, i).tiles;
+                n += kUnitTiles + block_of<kBlockRows, T::kKeys>(tp, q, i).tiles;
             n = wave_incl_sum_u64(n);
             if (lane == kWave - 1) s.before[b + 1] = n * p.Hkv;
         }
@@ -959,7 +1059,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         for (int i0 = 0; q.blocks > 1; i0 += kWave) {
             const int i = i0 + lane;
             const uint64_t n =
-                i < q.blocks ? (uint64_t)kUnitTiles + block_of<kBlockRows, T::kKeys>(p, q, i).tiles : 0;
+                i < q.blocks ? (uint64_t)kUnitTiles + block_of<kBlockRows, T::kKeys>(tp, q, i).tiles : 0;
             const uint64_t in64 = wave_incl_sum_u64(n);
             const uint64_t all = __shfl(in64, kWave - 1, kWave);
             if (rest < all || i0 + kWave >= q.blocks) {
@@ -975,17 +1075,18 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         next.head = __builtin_amdgcn_readfirstlane(head);
         next.blk = __builtin_amdgcn_readfirstlane(blk);
         next.q = scalar_request<kBlockRows>(p, next.b);
-        next.k = block_of<kBlockRows, T::kKeys>(p, next.q, next.blk);
+        next.k = block_of<kBlockRows, T::kKeys>(tp, next.q, next.blk);
         int place = __builtin_amdgcn_readfirstlane((int)rest) - kUnitTiles;
         if (place < 0) {
             cur -= (int64_t)place;
             place = 0;
         }
-        next.tile = next.k.tile + place;
-        next.left = next.k.tiles - (next.tile - next.k.tile);
+        next.tile = next.k.at(place);
+        next.left = next.k.tiles - place;
     }
     auto begin_next = [&](Unit &u) {
-        const AttendParams p = params_again().a;
+        const TileParams tp = params_again();
+        const AttendParams &p = tp.a;
         if (++u.blk == u.q.blocks) {
             u.blk = 0;
             if (++u.head == p.Hkv) {
@@ -994,8 +1095,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 while (u.q.blocks == 0);
             }
         }
-        u.k = block_of<kBlockRows, T::kKeys>(p, u.q, u.blk);
-        u.tile = u.k.tile;
+        u.k = block_of<kBlockRows, T::kKeys>(tp, u.q, u.blk);
+        u.tile = u.k.at(0);
         u.left = u.k.tiles;
     };
 
@@ -1016,8 +1117,11 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 begin_next(ahead);
                 T::enter(tp, sg, ahead);
                 T::look_up(tp, sg, ahead.tile);
-            } else if (++ahead.tile - sg.batch0 == kWave) {
-                T::look_up(tp, sg, ahead.tile);
+            } else {
+                const int tile = ahead.k.after(ahead.tile);
+                const bool jump = kTree && tile != ahead.tile + 1;
+                ahead.tile = tile;
+                if (jump || tile - sg.batch0 == kWave) T::look_up(tp, sg, tile);
             }
         }
     };
@@ -1051,11 +1155,11 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
             if constexpr (kWide) {
 #pragma unroll 1
                 for (int sub = 0; sub < T::kKeys / 32; sub += 2)
-                    T::template compute<2>(slots, number, tile, sub, p, t, st, lane);
+                    T::template compute<2>(slots, number, tile, sub, p, t, st, s, lane);
             } else {
 #pragma unroll 1
                 for (int i = 0; i < each; ++i)
-                    T::template compute<1>(slots, number, tile, kg * each + i, p, t, st, lane);
+                    T::template compute<1>(slots, number, tile, kg * each + i, p, t, st, s, lane);
             }
             if (part) {
                 const uint64_t *bad = s.bad[number];
@@ -1065,16 +1169,17 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 if (any) {
 #pragma unroll 1
                     for (int i = 0; i < each; ++i)
-                        T::add_bad(bad, tile, kg * each + i, p, t, st, lane);
+                        T::add_bad(bad, tile, kg * each + i, p, t, st, s, lane);
                 }
             }
         }
         if (kWide) stage((number + kSlots - 1) & (kSlots - 1), lane);
-        ++next.tile;
+        next.tile = next.k.after(next.tile);
     };
 
     auto begin = [&]() {
-        const AttendParams p = params_again().a;
+        const TileParams again = params_again();
+        const AttendParams &p = again.a;
         const int G = p.Hq / p.Hkv;
         const int m0 = next.blk * kBlockRows;
         rows = next.q.M - m0 < kBlockRows ? next.q.M - m0 : kBlockRows;
@@ -1109,6 +1214,23 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         const int m_last = (qt * 32 + 31 < rows - 1 ? qt * 32 + 31 : rows - 1) + m0;
         t.pos_max = next.q.ctx + m_last / G;
         t.active = kg < kgs && qt * 32 < rows;
+#if DSPARK_TREE
+        t.border = 0x7FFFFFFF;
+        t.sinks = again.v.sinks;
+        if (again.v.masks) {
+            t.border = next.q.ctx;
+            t.pos_min = next.k.first;
+            t.pos_max = next.k.final;
+            t.mask = again.v.masks + (valid ? row : next.q.start) * again.v.words;
+            uint64_t bits = 0;
+            if (valid) {
+                t.pos = next.q.ctx + depth_of(again.v.depths, row, j);
+                if (again.v.words <= 2)
+                    bits = t.mask[0] | (again.v.words > 1 ? (uint64_t)t.mask[1] << 32 : 0u);
+            }
+            s.bits[tid] = bits;  // this lane's alone
+        }
+#endif
         // a negative scale turns the queries' signs, none at all their values to 0
         const float scale = p.scale * p.c.k_scale;
         t.c = (scale == 0.f ? 1.f : fabsf(scale)) * kLog2e;
@@ -1128,8 +1250,20 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
             const bool here = !kPadded || ks * 16 + (lane >> 5) * 8 < p.D;
             if (valid && t.active && here) x[ks] = *reinterpret_cast<const u32x4 *>(src + ks * 16);
         }
+#if DSPARK_TREE
+        const int i0 = next.k.tiles - next.left, sink = next.k.sink;
+        const int s0 = i0 * T::kKeys, s1 = (i0 + n < sink ? i0 + n : sink) * T::kKeys;
+        const int w0 = i0 > sink ? i0 : sink;
+        const int k0 = next.k.at(w0) * T::kKeys, k1 = next.k.at(i0 + n) * T::kKeys;
+        const int end = s1 < t.hi ? s1 : t.hi;
+        t.hole = s0 < end && T::holes(p.c, t.table, s0, end, tp.together);
+        if (i0 + n > sink)  // the window's first tile may hold some of the sinks
+            t.hole |= T::holes(p.c, t.table, k0 > t.lo || k0 < t.sinks ? k0 : t.lo,
+                               k1 < t.hi ? k1 : t.hi, tp.together);
+#else
         const int k0 = next.tile * T::kKeys, k1 = (next.tile + n) * T::kKeys;
         t.hole = T::holes(p.c, t.table, k0 > t.lo ? k0 : t.lo, k1 < t.hi ? k1 : t.hi, tp.together);
+#endif
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
@@ -1377,7 +1511,7 @@ static int tile_head(int D, bool e4m3) {
     return D > 64 ? 128 : 64;
 }
 
-size_t attention_ws_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
+[[maybe_unused]] static size_t ws_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
     (void)B;
     const int head = tile_head(D, false);  // the same for either type of cache
     if (head == 0) return 256;
@@ -1393,7 +1527,7 @@ size_t attention_ws_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
 }
 
 template <int D, bool kE4m3>
-static hipError_t launch_tiles(const AttendParams &p, void *ws, hipStream_t s) {
+static hipError_t launch_tiles(const AttendParams &p, const TreeView &v, void *ws, hipStream_t s) {
     TileParams tp;
     tp.a = p;
     char *at = static_cast<char *>(ws);
@@ -1406,6 +1540,9 @@ static hipError_t launch_tiles(const AttendParams &p, void *ws, hipStream_t s) {
                   p.c.slot_stride * item * p.c.page < (1ll << 32);
     tp.page_bytes = (uint32_t)(p.c.page_stride * item);
     tp.slot_bytes = (uint32_t)(p.c.slot_stride * item);
+#if DSPARK_TREE
+    tp.v = v;
+#endif
     for (int b = 0; b < p.B; b += kGroupRequests) {
         tp.a.B = p.B - b < kGroupRequests ? p.B - b : kGroupRequests;
         tp.a.cu = p.cu + b;
@@ -1430,33 +1567,41 @@ static hipError_t launch_tiles(const AttendParams &p, void *ws, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <bool kTree>
-static hipError_t launch_rows(const AttendParams &p, const TreeView &v, bool e4m3, hipStream_t s) {
-    const dim3 grid((unsigned)p.rows, (unsigned)p.Hq);
-    if (e4m3)
-        hipLaunchKernelGGL((attend_row_kernel<true, kTree>), grid, dim3(kRowThreads), 0, s, p, v);
-    else
-        hipLaunchKernelGGL((attend_row_kernel<false, kTree>), grid, dim3(kRowThreads), 0, s, p, v);
-    return hipGetLastError();
-}
-
-hipError_t launch_attention(const AttendParams &p, bool e4m3, void *ws, hipStream_t s) {
+static hipError_t launch(const AttendParams &p, const TreeView &v, bool e4m3, void *ws,
+                         hipStream_t s) {
     // an 8-bit cache may be aligned to 8 bytes only
     const bool aligned = (((uintptr_t)p.c.k | (uintptr_t)p.c.v) % 16 == 0) &&
                          (!e4m3 || (p.c.page_stride | p.c.head_stride | p.c.slot_stride) % 16 == 0);
     switch (aligned ? tile_head(p.D, e4m3) : 0) {
     case 128:
-        return e4m3 ? launch_tiles<128, true>(p, ws, s) : launch_tiles<128, false>(p, ws, s);
+        return e4m3 ? launch_tiles<128, true>(p, v, ws, s) : launch_tiles<128, false>(p, v, ws, s);
     case 64:
-        return e4m3 ? launch_tiles<64, true>(p, ws, s) : launch_tiles<64, false>(p, ws, s);
+        return e4m3 ? launch_tiles<64, true>(p, v, ws, s) : launch_tiles<64, false>(p, v, ws, s);
     }
-    return launch_rows<false>(p, TreeView{}, e4m3, s);
+    const dim3 grid((unsigned)p.rows, (unsigned)p.Hq);
+    if (e4m3) hipLaunchKernelGGL((attend_row_kernel<true>), grid, dim3(kRowThreads), 0, s, p, v);
+    else hipLaunchKernelGGL((attend_row_kernel<false>), grid, dim3(kRowThreads), 0, s, p, v);
+    return hipGetLastError();
 }
+
+#if DSPARK_TREE
+}  // namespace trees
 
 hipError_t launch_tree_attention(const AttendParams &p, const TreeView &v, bool e4m3, void *ws,
                                  hipStream_t s) {
     if (!v.masks && v.sinks == 0) return launch_attention(p, e4m3, ws, s);
-    return launch_rows<true>(p, v, e4m3, s);
+    return trees::launch(p, v, e4m3, ws, s);
 }
+#else
+}  // namespace chains
+
+size_t attention_ws_bytes(int B, int max_rows, int Hq, int Hkv, int D) {
+    return chains::ws_bytes(B, max_rows, Hq, Hkv, D);
+}
+
+hipError_t launch_attention(const AttendParams &p, bool e4m3, void *ws, hipStream_t s) {
+    return chains::launch(p, TreeView{}, e4m3, ws, s);
+}
+#endif
 
 }  // namespace dspark
