@@ -212,6 +212,9 @@ constexpr int kHalfSlot = kSlotBytes / 2;
 constexpr int kGroupRequests = 512;  // of one launch; larger batches take several
 constexpr int kMinTiles = 1;  // per workgroup; one token at 4000 takes 21.5 us with 1, 22.5 with 2
 constexpr int kZeroBytes = 256;       // of the workspace that stay zero
+// kUnitTiles (below) of trees, whose cuts cost less: at 1, 2, 3, 4 and 5 128 trees took
+// 199, 186, 174, 173 and 170 us, four prompts in a window 269, 262, 250, 254 and 257 us.
+constexpr int kTreeUnitTiles = 4;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct TileParams {
@@ -225,7 +228,15 @@ struct TileParams {
     uint32_t page_bytes, slot_bytes;
 #if DSPARK_TREE
     TreeView v;
+    struct Split *splits;  // [wgs], of every workgroup
 #endif
+};
+
+// A unit that is cut after its first workgroup's tiles: its parts are in the slots of
+// workgroups first .. first + parts - 1. No parts where none is.
+struct Split {
+    int parts, first, rows, head, start, m0;
+    int pad[2];
 };
 
 // The call's parameters, read again from the kernel's arguments: for what runs once
@@ -256,8 +267,8 @@ __device__ __forceinline__ int scalar_load(const int32_t *p, int64_t i) {
 struct Request {
     int start, ctx, M, blocks;
 };
-template <int kBlockRows>
-__device__ __forceinline__ Request request_of(const AttendParams &p, int s, int e, int c) {
+__device__ __forceinline__ Request request_of(const AttendParams &p, int log_rows, int s, int e,
+                                              int c) {
     Request q;
     s = s < 0 ? 0 : (s > p.rows ? p.rows : s);
     e = e < s ? s : (e > p.rows ? p.rows : e);
@@ -265,17 +276,15 @@ __device__ __forceinline__ Request request_of(const AttendParams &p, int s, int 
     q.start = s;
     q.ctx = context_of(c);
     q.M = n * (p.Hq / p.Hkv);
-    q.blocks = (q.M + kBlockRows - 1) / kBlockRows;
+    q.blocks = (q.M + (1 << log_rows) - 1) >> log_rows;
     return q;
 }
-template <int kBlockRows>
-__device__ __forceinline__ Request load_request(const AttendParams &p, int b) {
-    return request_of<kBlockRows>(p, p.cu[b], p.cu[b + 1], p.ctx[b]);
+__device__ __forceinline__ Request load_request(const AttendParams &p, int log_rows, int b) {
+    return request_of(p, log_rows, p.cu[b], p.cu[b + 1], p.ctx[b]);
 }
-template <int kBlockRows>
-__device__ __forceinline__ Request scalar_request(const AttendParams &p, int b) {
-    return request_of<kBlockRows>(p, scalar_load(p.cu, b), scalar_load(p.cu, b + 1),
-                                  scalar_load(p.ctx, b));
+__device__ __forceinline__ Request scalar_request(const AttendParams &p, int log_rows, int b) {
+    return request_of(p, log_rows, scalar_load(p.cu, b), scalar_load(p.cu, b + 1),
+                      scalar_load(p.ctx, b));
 }
 // Positions [lo, hi) that block i of a request needs, its first and last row's
 // positions, and its tiles (one at least: a block that sees nothing still writes
@@ -303,12 +312,13 @@ struct Block {
 #endif
     }
 };
-template <int kBlockRows, int kKeys>
-__device__ __forceinline__ Block block_of(const TileParams &tp, const Request &q, int i) {
+template <int kKeys>
+__device__ __forceinline__ Block block_of(const TileParams &tp, int log_rows, const Request &q,
+                                          int i) {
     const AttendParams &p = tp.a;
     const int G = p.Hq / p.Hkv;
-    const int m0 = i * kBlockRows;
-    const int m1 = (q.M < m0 + kBlockRows ? q.M : m0 + kBlockRows) - 1;
+    const int m0 = i << log_rows;
+    const int m1 = (q.M < m0 + (1 << log_rows) ? q.M : m0 + (1 << log_rows)) - 1;
     const int64_t width = (int64_t)p.c.table_width * p.c.page;
     Block k;
     k.first = q.ctx + m0 / G;
@@ -395,7 +405,8 @@ struct Tiles {
     static constexpr int kWaves = kWide ? 8 : 4;
     static constexpr int kThreads = kWaves * kWave;
     static constexpr int kSlots = kWide ? 4 : 2;         // tiles in LDS
-    static constexpr int kBlockRows = kWide ? kWideRows : kNarrowRows;
+    static constexpr int kLogRows = kWide ? 8 : 7;  // query rows of a block
+    static_assert((kWide ? kWideRows : kNarrowRows) == 1 << kLogRows, "blocks");
     // What a unit costs beside its tiles (its queries, its first tile, joining and
     // storing its rows), in tiles: a unit has this many places, then its tiles. At 0,
     // 1, 2, 3 and 5 the mixed batch took 377, 346, 315, 307 and 313 us, four prompts
@@ -654,7 +665,9 @@ struct Tiles {
                                                    State &st, const Lds &s, int lane) {
         const int h = lane >> 5;
         const AttendParams cold = params_again().a;
-        const uint32_t bits = bits_of(s, t, tile * kKeys + sub * 32);
+#if DSPARK_TREE
+        const uint32_t bits = seen(p, s, t, tile * kKeys + sub * 32);
+#endif
 #pragma unroll 1
         for (int y = sub * 32; y < sub * 32 + 32; ++y) {
             if (!(bad[y / kWaveRows * kRowWords + y % kWaveRows / 64] >> (y % kWaveRows % 64) & 1))
@@ -662,7 +675,11 @@ struct Tiles {
             const int key = tile * kKeys + y;
             const int64_t at = slot_offset(cold.c, t.table, key, 0);
             if (at < 0) continue;
-            const bool see = visible(p, t, key, bits >> (y & 31) & 1);
+#if DSPARK_TREE
+            const bool see = bits >> (y & 31) & 1;
+#else
+            const bool see = visible(p, t, key);
+#endif
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -677,36 +694,41 @@ struct Tiles {
     }
 
     // ------------------------------------------------------------- compute
-    // Whether this lane's query row sees a position that has a page; `bit`: of its mask.
-    __device__ static __forceinline__ bool visible(const AttendParams &p, const Task &t, int key,
-                                                   bool bit) {
 #if DSPARK_TREE
-        const bool near = p.window == 0 || key > t.pos - p.window || key < t.sinks;
-        return key < t.hi && (key < t.border ? key <= t.pos && near : bit);
+    // Bits below n of 32.
+    __device__ static __forceinline__ uint32_t below(int n) {
+        return n >= 32 ? 0xFFFFFFFFu : (1u << (n < 0 ? 0 : n)) - 1u;
+    }
+    // The positions of 32 from k0 on that this lane's query row sees, if they have pages,
+    // as bits. The bits of the row's mask are kept in LDS: a load from memory would wait
+    // for the tiles on their way.
+    __device__ static __forceinline__ uint32_t seen(const AttendParams &p, const Lds &s,
+                                                    const Task &t, int k0) {
+        const int64_t past = (int64_t)k0 - t.border;  // the border is past all keys of a chain
+        uint32_t see = below(t.pos + 1 - k0);
+        if (past > -32) see &= below((int)-past);
+        if (p.window > 0) see &= ~below(t.pos + 1 - p.window - k0) | below(t.sinks - k0);
+        if (past > -32) {
+            const int words = params_again().v.words;
+            if (words <= 2) {
+                const uint64_t m = s.bits[threadIdx.x];
+                see |= past >= 64 ? 0u : (uint32_t)(past < 0 ? m << -past : m >> past);
+            } else {
+                const int w = (int)(past >> 5);
+                const uint64_t lo = w >= 0 && w < words ? t.mask[w] : 0u;
+                const uint64_t hi = w + 1 < words ? t.mask[w + 1] : 0u;
+                see |= (uint32_t)((lo | hi << 32) >> (past & 31));
+            }
+        }
+        return see & below(t.hi - k0);
+    }
 #else
+    // Whether this lane's query row sees a position that has a page.
+    __device__ static __forceinline__ bool visible(const AttendParams &p, const Task &t, int key) {
         return key <= t.pos && key >= t.lo && key < t.hi &&
                (p.window == 0 || key > t.pos - p.window);
-#endif
     }
-    // The bits of this lane's row for 32 positions from k0 on, 0 below the border. Kept in
-    // LDS: a load from memory would wait for the tiles on their way.
-    __device__ static __forceinline__ uint32_t bits_of(const Lds &s, const Task &t, int k0) {
-#if DSPARK_TREE
-        const int64_t base = (int64_t)k0 - t.border;
-        if (base <= -32) return 0;
-        const int words = params_again().v.words;
-        if (words <= 2) {
-            const uint64_t m = s.bits[threadIdx.x];
-            return base >= 64 ? 0u : (uint32_t)(base < 0 ? m << -base : m >> base);
-        }
-        const int w = (int)(base >> 5);
-        const uint64_t lo = w >= 0 && w < words ? t.mask[w] : 0u;
-        const uint64_t hi = w + 1 < words ? t.mask[w + 1] : 0u;
-        return (uint32_t)((lo | hi << 32) >> (base & 31));
-#else
-        return 0;
 #endif
-    }
     __device__ static __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
         const u32x4 x = {
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false)),
@@ -899,14 +921,20 @@ struct Tiles {
                 if (t.hole)
                     no = (uint32_t)__ballot(slot_offset(params_again().a.c, t.table,
                                                         k0 + i * 32 + (lane & 31), 0) < 0);
-                const uint32_t bits = bits_of(s, t, k0 + i * 32);
+#if DSPARK_TREE
+                // the half's own bits first: a constant place for every register then
+                const uint32_t bits = (seen(p, s, t, k0 + i * 32) & ~no) >> (4 * h);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    x[i][r] = bits & 1u << (8 * (r / 4) + (r & 3)) ? x[i][r] : -INFINITY;
+#else
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int y = 8 * (r / 4) + 4 * h + (r & 3);
-                    x[i][r] = visible(p, t, k0 + i * 32 + y, bits >> y & 1) && !(no >> y & 1)
-                                  ? x[i][r]
-                                  : -INFINITY;
+                    x[i][r] = visible(p, t, k0 + i * 32 + y) && !(no >> y & 1) ? x[i][r]
+                                                                               : -INFINITY;
                 }
+#endif
             }
         }
         float top = x[0][0];
@@ -973,9 +1001,14 @@ template <int D, bool kE4m3, bool kWide, bool kPadded>
 __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileParams tp) {
     using T = Tiles<D, kE4m3, kWide, kPadded>;
     using Unit = typename T::Unit;
-    constexpr int kBlockRows = T::kBlockRows, kSlots = T::kSlots, kWaveLoads = T::kWaveLoads;
+    constexpr int kSlots = T::kSlots, kWaveLoads = T::kWaveLoads;
     constexpr int kTileThreads = T::kThreads, kTileWaves = T::kWaves;
+#if DSPARK_TREE
+    constexpr int kUnitTiles = kTreeUnitTiles;
+#else
     constexpr int kUnitTiles = T::kUnitTiles;
+#endif
+    constexpr int log_rows = T::kLogRows, block_rows = 1 << log_rows;
     __shared__ typename T::Lds s;
     __shared__ __attribute__((aligned(1024))) char slot0[kSlotBytes];
     __shared__ __attribute__((aligned(1024))) char slot1[kSlotBytes];
@@ -988,18 +1021,18 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
 
     // places before every request
     if (tid == 0) s.before[0] = 0;
-    if ((int64_t)p.max_rows * G <= kBlockRows) {
+    if ((int64_t)p.max_rows * G <= block_rows) {
         for (int b = tid; b < p.B; b += kTileThreads) {
-            const Request q = load_request<kBlockRows>(p, b);
-            const int tiles = block_of<kBlockRows, T::kKeys>(tp, q, 0).tiles;
+            const Request q = load_request(p, log_rows, b);
+            const int tiles = block_of<T::kKeys>(tp, log_rows, q, 0).tiles;
             s.before[b + 1] = q.M > 0 ? (uint64_t)(kUnitTiles + tiles) * p.Hkv : 0;
         }
     } else {
         for (int b = wave; b < p.B; b += kTileWaves) {
-            const Request q = load_request<kBlockRows>(p, b);
+            const Request q = load_request(p, log_rows, b);
             uint64_t n = 0;
             for (int i = lane; i < q.blocks; i += kWave)
-                n += kUnitTiles + block_of<kBlockRows, T::kKeys>(tp, q, i).tiles;
+                n += kUnitTiles + block_of<T::kKeys>(tp, log_rows, q, i).tiles;
             n = wave_incl_sum_u64(n);
             if (lane == kWave - 1) s.before[b + 1] = n * p.Hkv;
         }
@@ -1028,17 +1061,67 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     }
     __syncthreads();
     const uint64_t total = s.before[p.B];
+#if DSPARK_TREE
+    // Where all requests have one block and about as many tiles (decoding and trees in
+    // a window), every workgroup gets as many whole units as another and none is cut:
+    // 64 trees in a window of 1024 take 62 us, 77 cut. Allowed to take 30 % longer than
+    // the even division by tiles, which is less than what its cuts cost.
+    bool whole_units = false;
+    if ((int64_t)p.max_rows * G <= block_rows) {
+        uint32_t most = 0;
+        bool all = true;
+        for (int b = tid; b < p.B; b += kTileThreads) {
+            const uint64_t n = s.before[b + 1] - s.before[b];
+            all &= n > 0;
+            const uint32_t places = (uint32_t)udiv64((int64_t)n, p.Hkv);
+            most = places > most ? places : most;
+        }
+        const uint64_t key = ((uint64_t)!__all(all) << 32) | wave_max_u64(most);
+        __syncthreads();
+        if (lane == 0) s.part[wave] = key;
+        __syncthreads();
+        uint64_t top = 0;
+        for (int i = 0; i < kTileWaves; ++i) top = s.part[i] > top ? s.part[i] : top;
+        const int units = p.B * p.Hkv, most_units = (units + wgs - 1) / wgs;
+        const uint64_t even = (uint64_t)udiv64((int64_t)total + wgs - 1, wgs);
+        whole_units = (top >> 32) == 0 && top * most_units * 10 <= even * 13;
+    }
+#endif
     uint64_t per = (uint64_t)udiv64((int64_t)total + wgs - 1, wgs);
     per = per < kMinTiles + kUnitTiles ? kMinTiles + kUnitTiles : per;  // so one tile at least
     // Workgroups go to the 8 XCDs in turn: each XCD takes one run of the tiles, so
     // that units of one head meet in one L2.
-    const int used = (int)udiv64((int64_t)(total + per - 1), (int64_t)per);
+    int used = (int)udiv64((int64_t)(total + per - 1), (int64_t)per);
+#if DSPARK_TREE
+    if (whole_units) used = p.B * p.Hkv < wgs ? p.B * p.Hkv : wgs;
+#endif
     const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
     const int share = used / 8 + (xcd < used % 8);
+#if DSPARK_TREE
+    Split split = {};
+    if (nth >= share) {
+        if (tid == 0) tp.splits[blockIdx.x] = split;
+        return;
+    }
+#else
     if (nth >= share) return;
+#endif
     const int g = xcd * (used / 8) + (xcd < used % 8 ? xcd : used % 8) + nth;
-    const uint64_t start = (uint64_t)g * per;
-    const uint64_t end = start + per < total ? start + per : total;
+    uint64_t start = (uint64_t)g * per;
+    uint64_t end = start + per < total ? start + per : total;
+#if DSPARK_TREE
+    if (whole_units) {
+        auto place_of = [&](int g) {
+            const int u = (int)udiv64((int64_t)g * (p.B * p.Hkv), used);
+            const int b = u / p.Hkv;
+            if (b == p.B) return total;
+            const uint64_t n = s.before[b + 1] - s.before[b];
+            return s.before[b] + (uint64_t)(u - b * p.Hkv) * (uint64_t)udiv64((int64_t)n, p.Hkv);
+        };
+        start = place_of(g);
+        end = place_of(g + 1);
+    }
+#endif
 
     // the unit of the first place, and the first tile at or after it
     Unit next;
@@ -1050,7 +1133,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
             if (s.before[mid + 1] <= start) b = mid + 1;
             else hi = mid;
         }
-        const Request q = load_request<kBlockRows>(p, b);
+        const Request q = load_request(p, log_rows, b);
         const uint64_t in = start - s.before[b];
         const uint64_t each = (uint64_t)udiv64((int64_t)(s.before[b + 1] - s.before[b]), p.Hkv);
         const int head = (int)udiv64((int64_t)in, (int64_t)each);
@@ -1059,7 +1142,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         for (int i0 = 0; q.blocks > 1; i0 += kWave) {
             const int i = i0 + lane;
             const uint64_t n =
-                i < q.blocks ? (uint64_t)kUnitTiles + block_of<kBlockRows, T::kKeys>(tp, q, i).tiles : 0;
+                i < q.blocks ? (uint64_t)kUnitTiles + block_of<T::kKeys>(tp, log_rows, q, i).tiles : 0;
             const uint64_t in64 = wave_incl_sum_u64(n);
             const uint64_t all = __shfl(in64, kWave - 1, kWave);
             if (rest < all || i0 + kWave >= q.blocks) {
@@ -1074,8 +1157,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         next.b = __builtin_amdgcn_readfirstlane(b);
         next.head = __builtin_amdgcn_readfirstlane(head);
         next.blk = __builtin_amdgcn_readfirstlane(blk);
-        next.q = scalar_request<kBlockRows>(p, next.b);
-        next.k = block_of<kBlockRows, T::kKeys>(tp, next.q, next.blk);
+        next.q = scalar_request(p, log_rows, next.b);
+        next.k = block_of<T::kKeys>(tp, log_rows, next.q, next.blk);
         int place = __builtin_amdgcn_readfirstlane((int)rest) - kUnitTiles;
         if (place < 0) {
             cur -= (int64_t)place;
@@ -1091,11 +1174,11 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
             u.blk = 0;
             if (++u.head == p.Hkv) {
                 u.head = 0;
-                do u.q = scalar_request<kBlockRows>(p, ++u.b);
+                do u.q = scalar_request(p, log_rows, ++u.b);
                 while (u.q.blocks == 0);
             }
         }
-        u.k = block_of<kBlockRows, T::kKeys>(tp, u.q, u.blk);
+        u.k = block_of<T::kKeys>(tp, log_rows, u.q, u.blk);
         u.tile = u.k.at(0);
         u.left = u.k.tiles;
     };
@@ -1181,8 +1264,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         const TileParams again = params_again();
         const AttendParams &p = again.a;
         const int G = p.Hq / p.Hkv;
-        const int m0 = next.blk * kBlockRows;
-        rows = next.q.M - m0 < kBlockRows ? next.q.M - m0 : kBlockRows;
+        const int m0 = next.blk << log_rows;
+        rows = next.q.M - m0 < block_rows ? next.q.M - m0 : block_rows;
         const uint64_t rest = end - cur;
         n = (uint64_t)next.left < rest ? next.left : (int)rest;
         // 32 query rows a wave; where fewer than eight waves hold them all, the
@@ -1332,7 +1415,31 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         const int g1 = (int)udiv64((int64_t)(unit + next.k.tiles - 1), (int64_t)per);
         const int64_t size = slot_floats(tp.slot_rows, D);
         auto slot_of = [&](int w) { return tp.slots + size * (2 * (int64_t)w + (w == g0)); };
-        const int m0 = next.blk * kBlockRows;
+        const int m0 = next.blk << log_rows;
+#if DSPARK_TREE
+        // left for join_kernel: nothing here waits for the stores
+        if (kg == 0 && t.active) {
+            float *to = slot_of(g);
+            if (lane < 32 && valid)
+                *reinterpret_cast<f32x2 *>(to + 2 * (qt * 32 + lane)) = f32x2{st.m, st.l};
+            to += 2 * tp.slot_rows + (int64_t)qt * (32 * D) + 4 * lane;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    if (valid) *reinterpret_cast<f32x4 *>(to + (d * 4 + r / 4) * (4 * kWave)) =
+                        f32x4{st.o[d][r], st.o[d][r + 1], st.o[d][r + 2], st.o[d][r + 3]};
+        }
+        if (next.left == next.k.tiles) {
+            split.parts = g1 - g0 + 1;
+            split.first = g0;
+            split.rows = rows;
+            split.head = next.head;
+            split.start = next.q.start;
+            split.m0 = m0;
+        }
+    };
+#else
         // pairs of elements in the order of the registers, a wave's 64 pairs together
         constexpr int kPairs = D / 4;  // of a lane
         if (kg == 0 && t.active) {
@@ -1463,6 +1570,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 sums(std::integral_constant<int, 1>(), std::integral_constant<int, 16>());
         }
     };
+#endif
 
     begin();
     int done = 0;  // tiles of the unit
@@ -1477,7 +1585,78 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         done = 0;
     }
     wait_loads<0>();  // nothing of this workgroup may land in LDS after it ends
+#if DSPARK_TREE
+    if (tid == 0) params_again().splits[blockIdx.x] = split;
+#endif
 }
+
+#if DSPARK_TREE
+// Joins the parts of cut units: a workgroup takes some blocks of 32 rows by 32
+// elements of a unit (every gridDim.y-th), a thread four elements of one row, eight
+// parts on their way, their maximum and sums carried along. Joined by the last
+// workgroup to arrive, as chains are, the parts of one tree of 60 nodes on 4000
+// positions took 53 of 81 us: a tree has many rows, and few workgroups joined them all.
+// A part whose row saw nothing has no maximum and holds zeros. One whose scores were
+// NaN has none either, but a sum and values that are NaN: no part is left out,
+// whatever its factor.
+constexpr int kJoinThreads = 256;
+template <int D, bool kPadded, int kAhead>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(TileParams tp) {
+    const Split u = tp.splits[blockIdx.x];
+    if (u.parts == 0) return;
+    const AttendParams &p = tp.a;
+    const int lane = threadIdx.x & (kWave - 1), r4 = threadIdx.x / kWave;
+    const int64_t size = slot_floats(tp.slot_rows, D);
+    const float *slots = tp.slots + size * 2 * (int64_t)u.first;
+    const int G = p.Hq / p.Hkv;
+    const int blocks = (u.rows + 31) / 32 * (D / 32);
+    for (int i = blockIdx.y; i < blocks; i += gridDim.y) {
+        const int qt = i / (D / 32), d = i % (D / 32);
+        const int row = qt * 32 + (lane & 31);
+        const int e = d * 32 + 8 * r4 + 4 * (lane >> 5);
+        if (row >= u.rows || (kPadded && e >= p.D)) continue;
+        const uint32_t at =
+            2 * tp.slot_rows + qt * (32 * D) + (d * 4 + r4) * (4 * kWave) + 4 * lane;
+        float top = -INFINITY, l = 0.f;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int w0 = 0; w0 < u.parts; w0 += kAhead) {
+            f32x2 ml[kAhead];
+            f32x4 y[kAhead];
+#pragma unroll
+            for (int w = 0; w < kAhead; ++w) {
+                // the first part lies in its workgroup's second slot
+                const int n = w0 + w < u.parts ? w0 + w : w0;
+                const float *x = slots + size * (2 * (int64_t)n + (n == 0));
+                ml[w] = *reinterpret_cast<const f32x2 *>(x + (uint32_t)(2 * row));
+                y[w] = *reinterpret_cast<const f32x4 *>(x + at);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // all loads first
+            float m1 = top;
+#pragma unroll
+            for (int w = 0; w < kAhead; ++w) m1 = fmaxf(m1, ml[w][0]);
+            const float keep = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(top - m1);
+            top = m1;
+            l *= keep;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] *= keep;
+#pragma unroll
+            for (int w = 0; w < kAhead; ++w) {
+                const bool one = w0 + w < u.parts;
+                const float f =
+                    ml[w][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[w][0] - top);
+                l += one ? f * ml[w][1] : 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] += one ? f * y[w][k] : 0.f;
+            }
+        }
+        const float norm = l > 0.f ? p.c.v_scale / l : 0.f;
+        const int mm = u.m0 + row, jj = mm / G, hh = u.head * G + (mm - jj * G);
+        uint16_t *o = p.out + ((int64_t)(u.start + jj) * p.Hq + hh) * (kPadded ? p.D : D) + e;
+        *reinterpret_cast<uint64_t *>(o) = (uint64_t)pack_bf16(v[0] * norm, v[1] * norm) |
+                                           ((uint64_t)pack_bf16(v[2] * norm, v[3] * norm) << 32);
+    }
+}
+#endif
 
 static int tile_wgs(bool wide) { return device_cu_count() * (wide ? 1 : 2); }
 // Calls whose requests may have over 128 query rows of a key-value head (prompts)
@@ -1503,6 +1682,7 @@ static int tile_slot_rows(int max_rows, int Hq, int Hkv) {
     return m >= kWideRows ? kWideRows : (int)((m + 31) / 32 * 32);
 }
 static size_t tile_arrival_bytes() { return ((size_t)tile_wgs(false) * 4 + 255) & ~(size_t)255; }
+static size_t tile_split_bytes() { return (size_t)tile_wgs(false) * sizeof(Split); }
 
 // The head size of the tiles for heads of D, 0 where they do not serve it: a row is
 // loaded 16 bytes at a time.
@@ -1523,7 +1703,7 @@ static int tile_head(int D, bool e4m3) {
     // A call may have fewer rows, and the kernel for those twice the workgroups.
     const int narrow = kNarrowRows / (Hq / Hkv);  // the most rows it takes
     if (tile_wide(max_rows, Hq, Hkv) && narrow > 0 && need(narrow) > slots) slots = need(narrow);
-    return (kZeroBytes + tile_arrival_bytes() + slots + 255) & ~(size_t)255;
+    return (kZeroBytes + tile_arrival_bytes() + tile_split_bytes() + slots + 255) & ~(size_t)255;
 }
 
 template <int D, bool kE4m3>
@@ -1533,7 +1713,8 @@ static hipError_t launch_tiles(const AttendParams &p, const TreeView &v, void *w
     char *at = static_cast<char *>(ws);
     tp.zeros = at;
     tp.arrivals = reinterpret_cast<unsigned *>(at + kZeroBytes);
-    tp.slots = reinterpret_cast<float *>(at + kZeroBytes + tile_arrival_bytes());
+    tp.slots = reinterpret_cast<float *>(at + kZeroBytes + tile_arrival_bytes() +
+                                         tile_split_bytes());
     tp.slot_rows = tile_slot_rows(p.max_rows, p.Hq, p.Hkv);
     const int64_t item = kE4m3 ? 1 : 2;
     tp.together = p.c.page % 16 == 0 && p.c.page_stride * item < (1ll << 32) &&
@@ -1542,6 +1723,7 @@ static hipError_t launch_tiles(const AttendParams &p, const TreeView &v, void *w
     tp.slot_bytes = (uint32_t)(p.c.slot_stride * item);
 #if DSPARK_TREE
     tp.v = v;
+    tp.splits = reinterpret_cast<Split *>(at + kZeroBytes + tile_arrival_bytes());
 #endif
     for (int b = 0; b < p.B; b += kGroupRequests) {
         tp.a.B = p.B - b < kGroupRequests ? p.B - b : kGroupRequests;
@@ -1553,6 +1735,22 @@ static hipError_t launch_tiles(const AttendParams &p, const TreeView &v, void *w
             hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3, kWide, kPadded>),
                                dim3(tile_wgs(kWide)),
                                dim3(Tiles<D, kE4m3, kWide, kPadded>::kThreads), 0, s, tp);
+#if DSPARK_TREE
+            // Few units are cut into many parts each: 16 of them read at once, by as many
+            // workgroups as a unit has blocks (one tree of 60 nodes: 42 us, 50 as below).
+            // Many are cut in two, mostly (128 trees: 176 us, 195 as above).
+            constexpr int kRows = 1 << Tiles<D, kE4m3, kWide, kPadded>::kLogRows;
+            const int64_t units = (int64_t)tp.a.B * p.Hkv *
+                                  (((int64_t)p.max_rows * (p.Hq / p.Hkv) + kRows - 1) / kRows);
+            const bool few = units * 4 < tile_wgs(kWide);
+            const dim3 shares(tile_wgs(kWide), few ? 32 : 16);
+            if (few)
+                hipLaunchKernelGGL((join_kernel<D, kPadded, 16>), shares, dim3(kJoinThreads), 0, s,
+                                   tp);
+            else
+                hipLaunchKernelGGL((join_kernel<D, kPadded, 2>), shares, dim3(kJoinThreads), 0, s,
+                                   tp);
+#endif
         };
         const std::true_type yes;
         const std::false_type no;
