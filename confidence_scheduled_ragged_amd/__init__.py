@@ -974,7 +974,7 @@ def dspark_fork_pages(table, held, refs, src, dst, lens, page_size, out=None):
     _need(dst, "dst", torch.int32, (n,), gpu)
     _need(src, "src", torch.int32, (n,), gpu)
     if out is None:
-        out = tuple(torch.empty_like(src) for _ in range(4))
+        out = src.new_empty((4, n)).unbind(0)
     for t, name in zip(out, ("copy_src", "copy_dst", "copy_slots", "granted")):
         _need(t, name, torch.int32, (n,), gpu)
     _launch(

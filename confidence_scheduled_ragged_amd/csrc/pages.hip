@@ -12,17 +12,10 @@ namespace dspark {
 
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWaves = kPoolThreads / kWave;
-constexpr int kPerThread = 16;  // entries of refs that a thread looks at together
+constexpr int kRefRows = 16;  // entries of refs that a thread looks at together
+constexpr int kPoolWords = kRefRows * kPoolWaves + 4;  // of LDS for scans
 constexpr int kMoveThreads = 128;
 constexpr int kCopyThreads = 256;
-
-// What threads of the workgroup have written is read anew afterwards, past the
-// vector cache: the atomics on refs do not go through it.
-__device__ __forceinline__ void pool_barrier() {
-    __threadfence();
-    __syncthreads();
-    __threadfence();
-}
 
 // Inclusive sum over the workgroup; `all` gets the total.
 __device__ __forceinline__ int pool_scan(int x, int *lds, int &all) {
@@ -48,55 +41,80 @@ __device__ __forceinline__ int clamped(int x, int lo, int hi) {
     return x < lo ? lo : (x > hi ? hi : x);
 }
 
-// Takes the lowest free pages from `from` (a multiple of the workgroup's share) on:
+// Takes the lowest free pages from `from` (a multiple of what is looked at together) on:
 // take(rank, page) is called for ranks 0 .. need - 1 as far as there are free pages.
 // Returns how many there were; `from` is left where the next search goes on.
+// Entries of refs are read past the vector cache, which the atomics on them do not go
+// through, 16 rows of 1024 at a time: a page's rank is a count of bits.
 template <typename Take>
 __device__ __forceinline__ int take_free(int32_t *refs, int pages, int &from, int need, int *lds,
                                          Take take) {
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     int found = 0;
     while (found < need && from < pages) {
-        const int p0 = from + threadIdx.x * kPerThread;
-        int32_t r[kPerThread];
-        int zeros = 0;
+        int32_t r[kRefRows];
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) r[i] = p0 + i < pages ? refs[p0 + i] : 1;
+        for (int i = 0; i < kRefRows; ++i) {
+            const int page = from + i * kPoolThreads + threadIdx.x;
+            r[i] = page < pages ? __hip_atomic_load(refs + page, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT)
+                                : 1;
+        }
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) zeros += r[i] == 0;
-        int all;
-        int rank = found + pool_scan(zeros, lds, all) - zeros;
+        for (int i = 0; i < kRefRows; ++i) {
+            const uint64_t free = __ballot(r[i] == 0);
+            if (lane == 0) lds[i * kPoolWaves + wave] = __popcll(free);
+        }
+        __syncthreads();
+        // the first 256 threads hold the counts of the waves' rows in the pages' order
+        static_assert(kRefRows * kPoolWaves == 4 * kWave, "four waves scan the counts");
+        int count = 0, in = 0;
+        if (wave < 4) {
+            count = lds[threadIdx.x];
+            in = wave_incl_scan(count, lane);
+            if (lane == kWave - 1) lds[kRefRows * kPoolWaves + wave] = in;
+        }
+        __syncthreads();
+        const int *sums = lds + kRefRows * kPoolWaves;
+        if (wave < 4) {
+            for (int w = 0; w < wave; ++w) in += sums[w];
+            lds[threadIdx.x] = in - count;
+        }
+        const int all = sums[0] + sums[1] + sums[2] + sums[3];
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            if (r[i] != 0) continue;
-            if (rank < need) {
-                refs[p0 + i] = 1;
-                take(rank, p0 + i);
+        for (int i = 0; i < kRefRows; ++i) {
+            const uint64_t free = __ballot(r[i] == 0);
+            const int rank = found + lds[i * kPoolWaves + wave] +
+                             __popcll(free & ((1ull << lane) - 1));
+            if (r[i] == 0 && rank < need) {
+                const int page = from + i * kPoolThreads + threadIdx.x;
+                refs[page] = 1;
+                take(rank, page);
             }
-            ++rank;
         }
         found += all;
-        if (found <= need) from += kPoolThreads * kPerThread;
+        if (found <= need) from += kPoolThreads * kRefRows;
     }
-    pool_barrier();
+    __syncthreads();
     return found < need ? found : need;
 }
 
-// The last index b of a non-decreasing LDS array [n] with before[b] <= x.
-__device__ __forceinline__ int owner(const int *before, int n, int x) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (before[mid] <= x) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+// The last index b of the non-decreasing before[kPoolThreads] in LDS with before[b] <= x.
+__device__ __forceinline__ int owner(const int *before, int x) {
+    int b = 0;
+#pragma unroll
+    for (int step = kPoolThreads / 2; step > 0; step >>= 1)
+        if (before[b + step] <= x) b += step;
+    return b;
 }
 
 // One workgroup, 1024 rows at a time: first every row's pages past its length are
 // released, then the rows that need more take theirs. Both work on the entries of
 // all rows laid end to end, so one long row costs no more than many short ones.
 __global__ __launch_bounds__(kPoolThreads) void resize_pages_kernel(PoolParams p) {
-    __shared__ int before_s[kPoolThreads], held_s[kPoolThreads], lds[kPoolWaves];
+    __shared__ int before_s[kPoolThreads], held_s[kPoolThreads], lds[kPoolWords];
     auto rows_from = [&](int b0, int &held, int &want) {
         const int b = b0 + threadIdx.x;
         held = want = 0;
@@ -106,30 +124,43 @@ __global__ __launch_bounds__(kPoolThreads) void resize_pages_kernel(PoolParams p
         const int64_t n = (len + p.page - 1) / p.page;
         want = n > p.width ? -1 : (int)n;  // more than a row can hold: not served
     };
+    int held = 0, want = 0;
     for (int b0 = 0; b0 < p.R; b0 += kPoolThreads) {
-        int held, want, all;
+        int all;
         rows_from(b0, held, want);
         const int less = want >= 0 && held > want ? held - want : 0;
         const int in = pool_scan(less, lds, all);
         before_s[threadIdx.x] = in - less;
         held_s[threadIdx.x] = want;
         __syncthreads();
-        for (int i = threadIdx.x; i < all; i += kPoolThreads) {
-            const int b = owner(before_s, kPoolThreads, i);
-            int32_t *e = p.table + (int64_t)(b0 + b) * p.width + held_s[b] + (i - before_s[b]);
-            release(p.refs, p.pages, *e);
-            *e = -1;
+        constexpr int kAhead = 8;  // entries on their way a thread
+        for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kPoolThreads) {
+            int32_t *e[kAhead];
+            int page[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * kPoolThreads < all ? i0 + u * kPoolThreads : i0;
+                const int b = owner(before_s, i);
+                e[u] = p.table + (int64_t)(b0 + b) * p.width + held_s[b] + (i - before_s[b]);
+                page[u] = *e[u];
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (i0 + u * kPoolThreads >= all) break;
+                release(p.refs, p.pages, page[u]);
+                *e[u] = -1;
+            }
         }
         if (less > 0) p.held[b0 + threadIdx.x] = want;
         if (b0 + (int)threadIdx.x < p.R) p.granted[b0 + threadIdx.x] = want >= 0;
         __syncthreads();
     }
-    pool_barrier();
+    __syncthreads();
     int from = 0;
     bool short_of = false;
     for (int b0 = 0; b0 < p.R; b0 += kPoolThreads) {
-        int held, want, all;
-        rows_from(b0, held, want);
+        int all;
+        if (p.R > kPoolThreads) rows_from(b0, held, want);
         const int more = want > held ? want - held : 0;
         const int in = pool_scan(more, lds, all);
         if (all == 0) continue;
@@ -137,7 +168,7 @@ __global__ __launch_bounds__(kPoolThreads) void resize_pages_kernel(PoolParams p
         held_s[threadIdx.x] = held;
         __syncthreads();
         auto entry = [&](int rank) {
-            const int b = owner(before_s, kPoolThreads, rank);
+            const int b = owner(before_s, rank);
             return p.table + (int64_t)(b0 + b) * p.width + held_s[b] + (rank - before_s[b]);
         };
         int got = 0;
@@ -149,7 +180,7 @@ __global__ __launch_bounds__(kPoolThreads) void resize_pages_kernel(PoolParams p
         if (more > 0 && served) p.held[b0 + threadIdx.x] = want;
         if (more > 0 && !served) p.granted[b0 + threadIdx.x] = 0;
         if (got < all) {  // that row gives back what it got
-            const int first = before_s[owner(before_s, kPoolThreads, got)];
+            const int first = before_s[owner(before_s, got)];
             for (int rank = first + threadIdx.x; rank < got; rank += kPoolThreads) {
                 int32_t *e = entry(rank);
                 release(p.refs, p.pages, *e);
@@ -157,14 +188,43 @@ __global__ __launch_bounds__(kPoolThreads) void resize_pages_kernel(PoolParams p
             }
             short_of = true;
         }
-        pool_barrier();
+        __syncthreads();
     }
 }
 
+// Positions of row s that fork i takes: at most what the row holds.
+__device__ __forceinline__ int64_t fork_length(const PoolParams &p, int s) {
+    const int64_t most = (int64_t)clamped(p.held[s], 0, p.width) * p.page;
+    const int64_t len = p.lens[s] < 0 ? 0 : p.lens[s];
+    return len < most ? len : most;
+}
+
+// Fork i by `threads` threads: the target's old pages go, the source's full pages and
+// the fresh one come. The source keeps its own hold on what is shared, so no page
+// looks free in between, whatever the order.
+__device__ __forceinline__ int fork_row(const PoolParams &p, int i, int tid, int threads) {
+    const int s = p.src[i], d = p.dst[i], fresh = p.copy_dst[i];
+    const int old = clamped(p.held[d], 0, p.width);
+    const int full = (int)(fork_length(p, s) / p.page), now = full + (fresh >= 0);
+    const int32_t *in = p.table + (int64_t)s * p.width;
+    int32_t *out = p.table + (int64_t)d * p.width;
+    const int last = now > old ? now : old;
+    for (int e = tid; e < last; e += threads) {
+        const int page = e < full ? in[e] : (e < now ? fresh : -1);
+        if (e < full && page >= 0 && page < p.pages) atomicAdd(p.refs + page, 1);
+        if (e < old) release(p.refs, p.pages, out[e]);
+        out[e] = page;
+    }
+    return now;
+}
+
 // One workgroup: which forks are granted, and a fresh page for each that ends
-// inside a page.
+// inside a page. kAll: and the forks themselves, a wave each.
+template <bool kAll>
 __global__ __launch_bounds__(kPoolThreads) void fork_plan_kernel(PoolParams p) {
-    __shared__ int src_s[kPoolThreads], dst_s[kPoolThreads], fresh_s[kPoolThreads], lds[kPoolWaves];
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    __shared__ i32x4 src_s[kPoolThreads / 4], dst_s[kPoolThreads / 4];
+    __shared__ int fresh_s[kPoolThreads], lds[kPoolWords];
     int from = 0;
     bool short_of = false;
     for (int i0 = 0; i0 < p.n; i0 += kPoolThreads) {
@@ -179,18 +239,22 @@ __global__ __launch_bounds__(kPoolThreads) void fork_plan_kernel(PoolParams p) {
         for (int k0 = 0; k0 < p.n; k0 += kPoolThreads) {
             const int k = k0 + threadIdx.x;
             __syncthreads();
-            src_s[threadIdx.x] = k < p.n ? p.src[k] : -1;
-            dst_s[threadIdx.x] = k < p.n ? p.dst[k] : -1;
+            reinterpret_cast<int *>(src_s)[threadIdx.x] = k < p.n ? p.src[k] : -1;
+            reinterpret_cast<int *>(dst_s)[threadIdx.x] = k < p.n ? p.dst[k] : -1;
             __syncthreads();
-            const int m = p.n - k0 < kPoolThreads ? p.n - k0 : kPoolThreads;
-            for (int u = 0; u < m; ++u) ok &= d != src_s[u] && (d != dst_s[u] || k0 + u >= i);
+            int m = p.n - k0 < kPoolThreads ? p.n - k0 : kPoolThreads;
+            if (!__any(i < p.n)) m = 0;
+#pragma unroll 4
+            for (int u = 0; u < m; u += 4) {
+                const i32x4 a = src_s[u / 4], z = dst_s[u / 4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)  // -1 past the last entry is no row
+                    ok &= d != a[v] && (d != z[v] || k0 + u + v >= i);
+            }
         }
         int part = -1, rest = 0;
         if (ok) {
-            const int held = clamped(p.held[s], 0, p.width);
-            const int64_t most = (int64_t)held * p.page;
-            int64_t len = p.lens[s] < 0 ? 0 : p.lens[s];
-            len = len < most ? len : most;
+            const int64_t len = fork_length(p, s);
             const int full = (int)(len / p.page);
             rest = (int)(len - (int64_t)full * p.page);
             if (rest > 0) part = p.table[(int64_t)s * p.width + full];
@@ -216,32 +280,24 @@ __global__ __launch_bounds__(kPoolThreads) void fork_plan_kernel(PoolParams p) {
         }
         short_of |= got < all;
     }
+    if constexpr (kAll) {
+        __syncthreads();
+        const int lane = threadIdx.x & (kWave - 1);
+        for (int i = threadIdx.x / kWave; i < p.n; i += kPoolWaves) {
+            if (!p.granted[i]) continue;
+            const int now = fork_row(p, i, lane, kWave);
+            if (lane == 0) p.held[p.dst[i]] = now;  // read by this wave only
+        }
+    }
 }
 
-// One workgroup per fork: the target's old pages go, the source's full pages and the
-// fresh one come. The source keeps its own hold on what is shared, so no page looks
-// free in between, whatever the order.
+// One workgroup per fork.
 __global__ __launch_bounds__(kPoolThreads) void fork_apply_kernel(PoolParams p) {
     const int i = blockIdx.x;
     if (!p.granted[i]) return;
-    const int s = p.src[i], d = p.dst[i], fresh = p.copy_dst[i];
-    if (s < 0 || s >= p.R || d < 0 || d >= p.R) return;
-    const int held = clamped(p.held[s], 0, p.width), old = clamped(p.held[d], 0, p.width);
-    const int64_t most = (int64_t)held * p.page;
-    int64_t len = p.lens[s] < 0 ? 0 : p.lens[s];
-    len = len < most ? len : most;
-    const int full = (int)(len / p.page), now = full + (fresh >= 0);
-    const int32_t *in = p.table + (int64_t)s * p.width;
-    int32_t *out = p.table + (int64_t)d * p.width;
-    const int last = now > old ? now : old;
-    for (int e = threadIdx.x; e < last; e += kPoolThreads) {
-        const int page = e < full ? in[e] : (e < now ? fresh : -1);
-        if (e < full && page >= 0 && page < p.pages) atomicAdd(p.refs + page, 1);
-        if (e < old) release(p.refs, p.pages, out[e]);
-        out[e] = page;
-    }
-    __syncthreads();  // every thread has read held[d]
-    if (threadIdx.x == 0) p.held[d] = now;
+    const int now = fork_row(p, i, threadIdx.x, kPoolThreads);
+    __syncthreads();  // every thread has read held
+    if (threadIdx.x == 0) p.held[p.dst[i]] = now;
 }
 
 // Copies `slots` slots of a page in every layer, keys and values: an item is one
@@ -340,7 +396,13 @@ hipError_t launch_resize_pages(const PoolParams &p, hipStream_t s) {
 }
 
 hipError_t launch_fork_pages(const PoolParams &p, hipStream_t s) {
-    hipLaunchKernelGGL(fork_plan_kernel, dim3(1), dim3(kPoolThreads), 0, s, p);
+    // A wave takes 1.5 us for every 64 entries of a row, a second launch 5 us: one launch
+    // for as many forks as waves, of short rows (three forks: 6 us, 9 with two).
+    if (p.n <= kPoolWaves && p.width <= 4 * kWave) {
+        hipLaunchKernelGGL((fork_plan_kernel<true>), dim3(1), dim3(kPoolThreads), 0, s, p);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((fork_plan_kernel<false>), dim3(1), dim3(kPoolThreads), 0, s, p);
     hipLaunchKernelGGL(fork_apply_kernel, dim3((unsigned)p.n), dim3(kPoolThreads), 0, s, p);
     return hipGetLastError();
 }
