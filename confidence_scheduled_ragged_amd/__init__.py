@@ -163,8 +163,7 @@ def dspark_workspace_bytes(B: int, gamma: int, V: int) -> int:
 
 def dspark_workspace_init(ws: torch.Tensor) -> None:
     _need(ws, "ws", torch.uint8)
-    _ok("dspark_workspace_init",
-        lib().dspark_workspace_init(_ptr(ws), ws.numel(), _stream(ws.device)))
+    _launch(ws.get_device(), "dspark_workspace_init", ws.data_ptr(), ws.numel())
 
 
 class _Kept:

@@ -169,8 +169,8 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p,
 // the resident workgroups, so any mix of long and short requests fills the chip, a
 // single long context included, and no launch shape depends on the lengths. A unit
 // that ends up in several workgroups leaves partial results (maximum, sum, weighted
-// values) in the workspace, and the last workgroup to arrive joins them in tile
-// order.
+// values) in the workspace; of a chain, the last workgroup to arrive joins them in
+// tile order, of trees, which have more rows, join_kernel does.
 //
 // Tiles are loaded from the pages straight into LDS, ahead of the tile at work and
 // whatever unit they belong to. Through registers, the loads alone took 326 of the
@@ -189,6 +189,13 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p,
 // TFLOP/s (99 us); in 8 bits these prompts take 347 us, since that kernel spills 25
 // registers, whose reloads wait behind the loads into LDS. Figures of one card;
 // others took 1 to 5 % more or less.
+//
+// Trees and sinks (DSPARK_TREE=1), time spent in the parts of 128 trees of 12 to 32
+// nodes, G = 4, 175 us in all: 2.2 to 2.7 us a tile and workgroup, 7 us a unit beside
+// its tiles (of which its queries 4, its rows' results 2), 1.3 us more for a tile that
+// is masked, 12 us before the first tile, 14 us for the join. Four trees of 64 nodes
+// on 41 to 113 thousand positions in 8 bits take 465 us, 807 TFLOP/s; one tree of 60
+// nodes on 4000 36 us, a chain of waits (10 us to the first tile, six tiles, the join).
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds 16 of a query's 32
 // scores of one MFMA (the other 16 sit in lane ^ 32), so the softmax needs one
@@ -707,7 +714,10 @@ struct Tiles {
         const int64_t past = (int64_t)k0 - t.border;  // the border is past all keys of a chain
         uint32_t see = below(t.pos + 1 - k0);
         if (past > -32) see &= below((int)-past);
-        if (p.window > 0) see &= ~below(t.pos + 1 - p.window - k0) | below(t.sinks - k0);
+        if (p.window > 0) {
+            const int64_t out = (int64_t)t.pos + 1 - p.window - k0;  // before the window
+            see &= ~below(out < 0 ? 0 : (int)(out < 32 ? out : 32)) | below(t.sinks - k0);
+        }
         if (past > -32) {
             const int words = params_again().v.words;
             if (words <= 2) {
@@ -1360,7 +1370,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     auto finish = [&]() {
         const TileParams tp = params_again();
         const AttendParams &p = tp.a;
-        const int G = p.Hq / p.Hkv;
+        [[maybe_unused]] const int G = p.Hq / p.Hkv;
         st.l = half_sum(st.l);
         // the groups of keys meet, 32 elements of all rows at a time
         for (int half = kWide ? 0 : kgs / 2; half >= 1; half /= 2) {

@@ -704,7 +704,7 @@ dspark_status check_pool(const int32_t *table, const int32_t *held, const int32_
     if (!table || !held || !lens || !refs) return DSPARK_ERR_NULL;
     if (R < 1 || R > DSPARK_MAX_TABLE_ROWS || width < 1 || page_size < 1 || pages < 1 ||
         pages > (1 << 30) || (long long)width * page_size > 0x7FFFFFFFll ||
-        (long long)R * width > (1ll << 40))
+        (long long)R * width > (1ll << 30))
         return DSPARK_ERR_SHAPE;
     if (misaligned(table, 4) || misaligned(held, 4) || misaligned(lens, 4) || misaligned(refs, 4))
         return DSPARK_ERR_ALIGN;

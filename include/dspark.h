@@ -643,7 +643,8 @@ dspark_status dspark_move_kv(void *k_cache, void *v_cache, int cache_type, int l
  * before more is appended to it.
  * table, held, refs int32 in and out; lens [R] int32; granted [R] int32 output.
  * DSPARK_ERR_SHAPE: R, width, page_size or pages below 1, R above
- * DSPARK_MAX_TABLE_ROWS, pages above 2^30, width * page_size above 2^31 - 1.
+ * DSPARK_MAX_TABLE_ROWS, pages or R * width above 2^30, width * page_size above
+ * 2^31 - 1.
  */
 dspark_status dspark_resize_pages(int32_t *table, int32_t *held, const int32_t *lens, int R,
                                   int width, int page_size, int32_t *refs, int pages,

@@ -346,3 +346,27 @@ def test_repeats_are_equal_and_on_another_stream():
         b = call(c, kc, vc, None)
     torch.cuda.synchronize()
     assert torch.equal(a[:c["cu"][-1]], b[:c["cu"][-1]])
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1),
+                                          (3, 2 ** 31 - 1), (2 ** 31 - 1, 5)])
+def test_the_largest_windows_and_sinks(window, sinks):
+    kw = dict(window=window, sinks=sinks)
+    c = make([20, 1, 90], [0, 130, 60], 4, 2, 128, 16, seed=2)
+    check(c, **kw)
+    check(tree(c, 3, **kw), **kw)
+    check(make([9], [40], 2, 1, 136, 16, seed=2), **kw)
+
+
+def test_heads_in_groups_past_a_block():
+    """One row of a key-value head fills more than a block of query rows."""
+    check(tree(make([5, 1, 3], [40, 100, 0], 300, 1, 64, 16, seed=4), 2))
+    check(make([2, 1], [90, 700], 130, 1, 64, 16, seed=4), window=60, sinks=70)
+
+
+def test_equal_units_are_not_cut():
+    """As many units as workgroups and more, all alike, in a window: whole ones each."""
+    for n, B, Hkv in ((1, 128, 8), (3, 70, 8), (2, 300, 2)):
+        c = make([n] * B, [90 + b % 7 for b in range(B)], Hkv, Hkv, 64, 16, seed=B)
+        check(c, window=64, sinks=4)
+        check(tree(c, 1, 64, 4), window=64, sinks=4)

@@ -144,6 +144,7 @@ TABLE_REFUSALS = [
     (dict(granted=0), ENULL), (dict(R=0), ESHAPE), (dict(R=(1 << 20) + 1), ESHAPE),
     (dict(width=0), ESHAPE), (dict(page=0), ESHAPE), (dict(pages=0), ESHAPE),
     (dict(pages=(1 << 30) + 1), ESHAPE), (dict(width=1 << 20, page=1 << 11), ESHAPE),
+    (dict(R=1 << 20, width=(1 << 10) + 1), ESHAPE),
     (dict(table=A + 2), EALIGN), (dict(held=A + 1), EALIGN), (dict(lens=A + 2), EALIGN),
     (dict(refs=A + 2), EALIGN), (dict(granted=A + 2), EALIGN)]
 
