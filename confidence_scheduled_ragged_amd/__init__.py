@@ -875,13 +875,15 @@ def dspark_tree_accept(packed_choice, packed_tokens, parents, cu_seqlens, max_ro
         raise ValueError("packed_choice, packed_tokens and parents must have one entry a row")
     _need(cu_seqlens, "cu_seqlens", torch.int32, None, gpu)
     B = cu_seqlens.numel() - 1
-    acc, bonus, path = (None, None, None) if out is None else out
-    acc = torch.empty(B, dtype=torch.int32, device=dev) if acc is None else acc
-    bonus = torch.empty(B, dtype=torch.int32, device=dev) if bonus is None else bonus
-    path = torch.empty((B, width), dtype=torch.int32, device=dev) if path is None else path
-    _need(acc, "accepted", torch.int32, (B,), gpu)
-    _need(bonus, "bonus", torch.int32, (B,), gpu)
-    _need(path, "path", torch.int32, (B, width), gpu)
+    if out is None:
+        acc, bonus, path = torch.empty(B * (width + 2), dtype=torch.int32, device=dev).split(
+            (B, B, B * width))
+        path = path.view(B, width)
+    else:
+        acc, bonus, path = out
+        _need(acc, "accepted", torch.int32, (B,), gpu)
+        _need(bonus, "bonus", torch.int32, (B,), gpu)
+        _need(path, "path", torch.int32, (B, width), gpu)
     _launch(
         gpu, "dspark_tree_accept",
         packed_choice.data_ptr(), packed_tokens.data_ptr(), parents.data_ptr(),

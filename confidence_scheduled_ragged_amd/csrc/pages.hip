@@ -101,13 +101,25 @@ __device__ __forceinline__ int take_free(int32_t *refs, int pages, int &from, in
     return found < need ? found : need;
 }
 
-// The last index b of the non-decreasing before[kPoolThreads] in LDS with before[b] <= x.
-__device__ __forceinline__ int owner(const int *before, int x) {
-    int b = 0;
+// For each x[u] the last index b[u] of the non-decreasing before[kPoolThreads] in LDS
+// with before[b[u]] <= x[u], step by step for all of them.
+template <int kN>
+__device__ __forceinline__ void owners(const int *before, const int (&x)[kN], int (&b)[kN]) {
 #pragma unroll
-    for (int step = kPoolThreads / 2; step > 0; step >>= 1)
-        if (before[b + step] <= x) b += step;
-    return b;
+    for (int u = 0; u < kN; ++u) b[u] = 0;
+#pragma unroll
+    for (int step = kPoolThreads / 2; step > 0; step >>= 1) {
+        int y[kN];
+#pragma unroll
+        for (int u = 0; u < kN; ++u) y[u] = before[b[u] + step];
+#pragma unroll
+        for (int u = 0; u < kN; ++u) b[u] += y[u] <= x[u] ? step : 0;
+    }
+}
+__device__ __forceinline__ int owner(const int *before, int x) {
+    int xs[1] = {x}, b[1];
+    owners(before, xs, b);
+    return b[0];
 }
 
 // One workgroup, 1024 rows at a time: first every row's pages past its length are
@@ -136,12 +148,15 @@ __global__ __launch_bounds__(kPoolThreads) void resize_pages_kernel(PoolParams p
         constexpr int kAhead = 8;  // entries on their way a thread
         for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kPoolThreads) {
             int32_t *e[kAhead];
-            int page[kAhead];
+            int page[kAhead], i[kAhead], b[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                i[u] = i0 + u * kPoolThreads < all ? i0 + u * kPoolThreads : i0;
+            owners(before_s, i, b);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + u * kPoolThreads < all ? i0 + u * kPoolThreads : i0;
-                const int b = owner(before_s, i);
-                e[u] = p.table + (int64_t)(b0 + b) * p.width + held_s[b] + (i - before_s[b]);
+                e[u] = p.table + (int64_t)(b0 + b[u]) * p.width + held_s[b[u]] +
+                       (i[u] - before_s[b[u]]);
                 page[u] = *e[u];
             }
 #pragma unroll
