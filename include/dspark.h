@@ -49,7 +49,8 @@
  *                       V < 1, or B*(gamma+1) above DSPARK_MAX_ROWS;
  *     DSPARK_ERR_ARG    a bad mode, a negative budget, a non-finite bias;
  *     DSPARK_ERR_ALIGN  a pointer misaligned for its element type
- *                       (2 bytes bf16, 4 bytes fp32/int32, 16 bytes ws);
+ *                       (2 bytes bf16, 4 bytes fp32/int32, 16 bytes ws; 1 byte
+ *                       for 8-bit caches);
  *     DSPARK_ERR_WORKSPACE  ws_bytes below dspark_workspace_bytes();
  *     DSPARK_ERR_HIP    a kernel launch failed (hipGetLastError).
  * - Device data is never validated on the host (that would need a sync).
