@@ -169,3 +169,18 @@ def test_copy_in_a_pool_past_32_bits():
         assert bool((x[:, pages - 1] == value).all())
     del k, v, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("n", [1, 16, 17, 40])
+@pytest.mark.parametrize("width", [200, 256, 257, 700])
+def test_forks_of_long_rows(n, width):
+    """As many forks as one launch takes and more, rows of as many pages and more."""
+    pool, state = both(3 * width + 2 * n + 9, n + 3, width, 4)
+    lens = [4 * width - 1, 2 * width, 4 * width - 6] + [0] * n
+    dspark.dspark_resize_pages(*state, i32(lens), 4)
+    pool.resize(lens)
+    src, dst = [i % 3 for i in range(n)], list(range(3, n + 3))
+    for at in (lens, [4 * width, 9, 4 * width - 6] + [0] * n):
+        got = dspark.dspark_fork_pages(*state, i32(src), i32(dst), i32(at), 4)
+        assert list(zip(*[x.tolist() for x in got])) == pool.fork(src, dst, at)
+        same(pool, state)

@@ -370,3 +370,48 @@ def test_equal_units_are_not_cut():
         c = make([n] * B, [90 + b % 7 for b in range(B)], Hkv, Hkv, 64, 16, seed=B)
         check(c, window=64, sinks=4)
         check(tree(c, 1, 64, 4), window=64, sinks=4)
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    """Calls on two streams, their contexts split over the device and joined."""
+    cases = [tree(make([40, 1], [3000, 9000], 8, 2, 128, 16, seed=s), s) for s in (1, 2)]
+    args = [(c["q"].to(DEV), *pools(c, DEV), i32(c["cu"]), i32(c["ctx"]), c["table"].to(DEV), 40)
+            for c in cases]
+    kws = [dict(depths=i32(c["depths"]), masks=i32(words_of(c["bits"], c["words"]))) for c in cases]
+    want = [dspark.dspark_tree_attention(*a, **k)[:41].clone() for a, k in zip(args, kws)]
+    need = dspark.dspark_attention_workspace_bytes(2, 40, 8, 2, 128)
+    ws = [torch.zeros(need, dtype=torch.uint8, device=DEV) for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(dspark.dspark_tree_attention(*args[i], ws=ws[i], **kws[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x[:41], want[i]) for x in got[i])
+
+
+def test_two_graphs_share_a_workspace():
+    """Graphs of calls of different sizes, replayed in turn with eager calls between."""
+    cases = [tree(make([n, 3], [2500, 700], 8, 2, 128, 16, seed=n), n) for n in (30, 64)]
+    graphs = []
+    for c in cases:
+        args = (c["q"].to(DEV), *pools(c, DEV), i32(c["cu"]), i32(c["ctx"]), c["table"].to(DEV),
+                c["max_rows"])
+        kw = dict(depths=i32(c["depths"]), masks=i32(words_of(c["bits"], c["words"])))
+        want = dspark.dspark_tree_attention(*args, **kw).clone()
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            dspark.dspark_tree_attention(*args, out=out, **kw)
+        graphs.append((graph, args, kw, out, want, c["cu"][-1]))
+    for _ in range(3):
+        for graph, args, kw, out, want, n in graphs:
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out[:n], want[:n])
+            assert torch.equal(dspark.dspark_tree_attention(*args, **kw)[:n], want[:n])
