@@ -235,12 +235,14 @@ struct TileParams {
     uint32_t page_bytes, slot_bytes;
 #if DSPARK_TREE
     TreeView v;
-    struct Split *splits;  // [wgs], of every workgroup
+    struct Split *splits;  // of every unit, or of every workgroup: [wgs] at most
+    int blocks;            // the most of a request, where there is one for every unit; or 0
 #endif
 };
 
 // A unit that is cut after its first workgroup's tiles: its parts are in the slots of
-// workgroups first .. first + parts - 1. No parts where none is.
+// workgroups first .. first + parts - 1. No parts where none is. Few units have one
+// each, of many each workgroup has one, for the unit that it is the first to cut.
 struct Split {
     int parts, first, rows, head, start, m0;
     int pad[2];
@@ -1109,9 +1111,19 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     const int share = used / 8 + (xcd < used % 8);
 #if DSPARK_TREE
     Split split = {};
-    if (nth >= share) {
-        if (tid == 0) tp.splits[blockIdx.x] = split;
-        return;
+    if (tp.blocks == 0) {
+        if (nth >= share) {
+            if (tid == 0) tp.splits[blockIdx.x] = split;
+            return;
+        }
+    } else {
+        if (blockIdx.x == 0)  // units that requests with fewer rows do not have
+            for (int i = tid; i < p.B * tp.blocks; i += kTileThreads) {
+                const int b = i / tp.blocks;
+                if (i - b * tp.blocks < load_request(p, log_rows, b).blocks) continue;
+                for (int h = 0; h < p.Hkv; ++h) tp.splits[i * p.Hkv + h].parts = 0;
+            }
+        if (nth >= share) return;
     }
 #else
     if (nth >= share) return;
@@ -1402,6 +1414,12 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
                 }
             }
         }
+#if DSPARK_TREE
+        Split *const own = tp.blocks == 0
+                               ? nullptr
+                               : tp.splits + (next.b * tp.blocks + next.blk) * p.Hkv + next.head;
+        if (own && tid == 0 && n == next.k.tiles) own->parts = 0;
+#endif
         if (n == next.k.tiles) {
             if (kg == 0 && t.active && valid) {
                 const float norm = st.l > 0.f ? p.c.v_scale / st.l : 0.f;
@@ -1447,6 +1465,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
             split.head = next.head;
             split.start = next.q.start;
             split.m0 = m0;
+            if (own && tid == 0) *own = split;
         }
     };
 #else
@@ -1596,7 +1615,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     }
     wait_loads<0>();  // nothing of this workgroup may land in LDS after it ends
 #if DSPARK_TREE
-    if (tid == 0) params_again().splits[blockIdx.x] = split;
+    const TileParams again = params_again();
+    if (tid == 0 && again.blocks == 0) again.splits[blockIdx.x] = split;
 #endif
 }
 
@@ -1742,6 +1762,14 @@ static hipError_t launch_tiles(const AttendParams &p, const TreeView &v, void *w
         tp.a.c.table = p.c.table + (int64_t)b * p.c.table_width;
         auto go = [&](auto wide, auto padded) {
             constexpr bool kWide = decltype(wide)::value, kPadded = decltype(padded)::value;
+#if DSPARK_TREE
+            constexpr int kRows = 1 << Tiles<D, kE4m3, kWide, kPadded>::kLogRows;
+            const int64_t most = (int64_t)p.max_rows * (p.Hq / p.Hkv);
+            const int64_t units = (int64_t)tp.a.B * p.Hkv * ((most + kRows - 1) / kRows);
+            const bool few = units * 4 < tile_wgs(kWide);
+            const int rows = (int)(most < kRows ? most : kRows);
+            tp.blocks = few ? (int)((most + kRows - 1) / kRows) : 0;
+#endif
             hipLaunchKernelGGL((attend_tile_kernel<D, kE4m3, kWide, kPadded>),
                                dim3(tile_wgs(kWide)),
                                dim3(Tiles<D, kE4m3, kWide, kPadded>::kThreads), 0, s, tp);
@@ -1749,17 +1777,14 @@ static hipError_t launch_tiles(const AttendParams &p, const TreeView &v, void *w
             // Few units are cut into many parts each: 16 of them read at once, by as many
             // workgroups as a unit has blocks (one tree of 60 nodes: 42 us, 50 as below).
             // Many are cut in two, mostly (128 trees: 176 us, 195 as above).
-            constexpr int kRows = 1 << Tiles<D, kE4m3, kWide, kPadded>::kLogRows;
-            const int64_t units = (int64_t)tp.a.B * p.Hkv *
-                                  (((int64_t)p.max_rows * (p.Hq / p.Hkv) + kRows - 1) / kRows);
-            const bool few = units * 4 < tile_wgs(kWide);
-            const dim3 shares(tile_wgs(kWide), few ? 32 : 16);
+            const int all = (rows + 31) / 32 * (D / 32);
             if (few)
-                hipLaunchKernelGGL((join_kernel<D, kPadded, 16>), shares, dim3(kJoinThreads), 0, s,
-                                   tp);
+                hipLaunchKernelGGL((join_kernel<D, kPadded, 16>), dim3((unsigned)units, all),
+                                   dim3(kJoinThreads), 0, s, tp);
             else
-                hipLaunchKernelGGL((join_kernel<D, kPadded, 2>), shares, dim3(kJoinThreads), 0, s,
-                                   tp);
+                hipLaunchKernelGGL((join_kernel<D, kPadded, 2>),
+                                   dim3(tile_wgs(kWide), all < 16 ? all : 16),
+                                   dim3(kJoinThreads), 0, s, tp);
 #endif
         };
         const std::true_type yes;
@@ -1797,7 +1822,6 @@ static hipError_t launch(const AttendParams &p, const TreeView &v, bool e4m3, vo
 
 hipError_t launch_tree_attention(const AttendParams &p, const TreeView &v, bool e4m3, void *ws,
                                  hipStream_t s) {
-    if (!v.masks && v.sinks == 0) return launch_attention(p, e4m3, ws, s);
     return trees::launch(p, v, e4m3, ws, s);
 }
 #else

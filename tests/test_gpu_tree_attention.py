@@ -111,16 +111,19 @@ def test_prompts_with_sinks():
 
 
 def test_a_chain_without_sinks_is_dspark_verify_attention():
+    """By definition: either lies within the bound of the 64-bit result."""
     for rows in ([17, 1, 5], [100, 300, 2]):
         c = make(rows, [3000, 900, 40], 8, 2, 128, 16, seed=10)
         kc, vc = pools(c, DEV)
         for window in (0, 50, 2000):
-            args = (c["q"].to(DEV), kc, vc, i32(c["cu"]), i32(c["ctx"]), c["table"].to(DEV),
-                    c["max_rows"])
-            a = dspark.dspark_verify_attention(*args, window=window)
-            b = dspark.dspark_tree_attention(*args, window=window)
-            n = c["cu"][-1]
-            assert torch.equal(a[:n], b[:n])
+            check(c, window=window)
+            out = torch.randn((c["cap"], 8, 128)).bfloat16()
+            want, tol = ref.attend(c["q"], c["kc"], c["vc"], c["cu"], c["ctx"], c["table"],
+                                   c["max_rows"], window=window, out=out)
+            got = dspark.dspark_verify_attention(c["q"].to(DEV), kc, vc, i32(c["cu"]), i32(c["ctx"]),
+                                                 c["table"].to(DEV), c["max_rows"], window=window,
+                                                 out=out.to(DEV))
+            assert bool(((got.cpu().double() - want).abs() <= tol).all())
 
 
 def any_masks(c, seed, density=0.5, words=None):
@@ -326,14 +329,30 @@ def test_graph_replays_with_new_trees():
 
 
 def test_both_attentions_share_a_workspace():
+    """Chains and trees in turn, split and joined: each as before."""
     c = make([17, 1, 5], [3000, 900, 40], 8, 2, 128, 16, seed=10)
     t = tree(make([30, 60], [2000, 9000], 8, 2, 128, 16, seed=11), 1)
+    args = (c["q"].to(DEV), *pools(c, DEV), i32(c["cu"]), i32(c["ctx"]), c["table"].to(DEV), 17)
+    first = dspark.dspark_verify_attention(*args)[:23].clone()
     for _ in range(3):
         check(t)
         check(c, window=500, sinks=9)
-        args = (c["q"].to(DEV), *pools(c, DEV), i32(c["cu"]), i32(c["ctx"]), c["table"].to(DEV), 17)
-        a = dspark.dspark_verify_attention(*args)
-        assert torch.equal(a[:23], dspark.dspark_tree_attention(*args)[:23])
+        check(c)
+        assert torch.equal(dspark.dspark_verify_attention(*args)[:23], first)
+
+
+def test_requests_without_rows_among_few_units():
+    """Their units are none: nothing is joined for them, whatever the workspace held."""
+    big = tree(make([60, 64], [9000, 4000], 8, 2, 128, 16, seed=1), 1)
+    for rows in ([0, 9], [5, 0, 0], [0, 0], [64, 0, 1]):
+        check(big)
+        c = make(rows, [700] * len(rows), 8, 2, 128, 16, seed=2)
+        c["max_rows"] = 64
+        check(tree(c, 2) if any(rows) else c, window=300, sinks=2)
+    wide = make([500, 0, 3], [300, 9, 5000], 4, 1, 64, 16, seed=3)
+    check(wide)
+    check(make([3, 0, 500], [9000, 9, 20], 4, 1, 64, 16, seed=4))
+    check(wide, window=100, sinks=70)
 
 
 def test_repeats_are_equal_and_on_another_stream():
