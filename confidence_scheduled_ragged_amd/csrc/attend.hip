@@ -193,9 +193,9 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p,
 // Trees and sinks (DSPARK_TREE=1), time spent in the parts of 128 trees of 12 to 32
 // nodes, G = 4, 175 us in all: 2.2 to 2.7 us a tile and workgroup, 7 us a unit beside
 // its tiles (of which its queries 4, its rows' results 2), 1.3 us more for a tile that
-// is masked, 12 us before the first tile, 14 us for the join. Four trees of 64 nodes
-// on 41 to 113 thousand positions in 8 bits take 465 us, 807 TFLOP/s; one tree of 60
-// nodes on 4000 36 us, a chain of waits (10 us to the first tile, six tiles, the join).
+// is masked, 12 us before the first tile, 15 us for the join. Four trees of 64 nodes
+// on 41 to 113 thousand positions in 8 bits take 467 us, 802 TFLOP/s; one tree of 60
+// nodes on 4000 32 us, a chain of waits (10 us to the first tile, six tiles, the join).
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds 16 of a query's 32
 // scores of one MFMA (the other 16 sit in lane ^ 32), so the softmax needs one
@@ -1774,9 +1774,10 @@ static hipError_t launch_tiles(const AttendParams &p, const TreeView &v, void *w
                                dim3(tile_wgs(kWide)),
                                dim3(Tiles<D, kE4m3, kWide, kPadded>::kThreads), 0, s, tp);
 #if DSPARK_TREE
-            // Few units are cut into many parts each: 16 of them read at once, by as many
-            // workgroups as a unit has blocks (one tree of 60 nodes: 42 us, 50 as below).
-            // Many are cut in two, mostly (128 trees: 176 us, 195 as above).
+            // Few units are cut into many parts each, of which 16 are read at once (one
+            // tree of 60 nodes: 42 us, 50 with two). Many are cut in two, mostly (128
+            // trees: 176 us, 195 with 16). A workgroup for every block of few units, where
+            // one for every workgroup of the tiles' kernel took 36 us for that tree, 32 so.
             const int all = (rows + 31) / 32 * (D / 32);
             if (few)
                 hipLaunchKernelGGL((join_kernel<D, kPadded, 16>), dim3((unsigned)units, all),
