@@ -731,7 +731,8 @@ def _attend(name, tree, q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, 
     qs = _packed_heads(q, "q", rows, Hq, D, gpu)
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
+    else:
+        _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
     max_rows = min(int(max_rows), rows)
     view = ()
     if tree is not None:
@@ -827,12 +828,14 @@ def dspark_tree_masks(parents, cu_seqlens, max_rows, ctx_lens=None, window=0, si
     depths, masks = (None, None) if out is None else out
     if depths is None:
         depths = torch.zeros(rows, dtype=torch.int32, device=parents.device)
+    else:
+        _need(depths, "depths", torch.int32, (rows,), gpu)
     if masks is None:
         masks = torch.zeros((rows, max(words, 1)), dtype=torch.int32, device=parents.device)
-    _need(depths, "depths", torch.int32, (rows,), gpu)
-    _need(masks, "masks", torch.int32, None, gpu)
-    if masks.dim() != 2 or masks.shape[0] != rows:
-        raise ValueError(f"masks must have shape ({rows}, words)")
+    else:
+        _need(masks, "masks", torch.int32, None, gpu)
+        if masks.dim() != 2 or masks.shape[0] != rows:
+            raise ValueError(f"masks must have shape ({rows}, words)")
     _launch(
         gpu, "dspark_tree_masks",
         parents.data_ptr(), cu_seqlens.data_ptr(), None if ctx_lens is None else ctx_lens.data_ptr(),
@@ -956,8 +959,10 @@ def dspark_resize_pages(table, held, refs, lens, page_size, granted=None):
     refs [pages], all changed in place). Returns granted [R] int32: 1 where the row
     holds what its length needs, 0 where there were too few free pages or places."""
     gpu, R, width = _pool(table, held, refs, lens)
-    granted = torch.empty_like(held) if granted is None else granted
-    _need(granted, "granted", torch.int32, (R,), gpu)
+    if granted is None:
+        granted = torch.empty_like(held)
+    else:
+        _need(granted, "granted", torch.int32, (R,), gpu)
     _launch(gpu, "dspark_resize_pages", table.data_ptr(), held.data_ptr(), lens.data_ptr(), R,
             width, int(page_size), refs.data_ptr(), refs.numel(), granted.data_ptr())
     return granted
@@ -970,14 +975,14 @@ def dspark_fork_pages(table, held, refs, src, dst, lens, page_size, out=None):
     what dspark_copy_pages takes to fill those pages. Rows that cannot be served have
     granted 0 and stay as they were."""
     gpu, R, width = _pool(table, held, refs, lens)
-    _need(src, "src", torch.int32, None, gpu)
     n = src.numel()
-    _need(dst, "dst", torch.int32, (n,), gpu)
     _need(src, "src", torch.int32, (n,), gpu)
+    _need(dst, "dst", torch.int32, (n,), gpu)
     if out is None:
         out = src.new_empty((4, n)).unbind(0)
-    for t, name in zip(out, ("copy_src", "copy_dst", "copy_slots", "granted")):
-        _need(t, name, torch.int32, (n,), gpu)
+    else:
+        for t, name in zip(out, ("copy_src", "copy_dst", "copy_slots", "granted")):
+            _need(t, name, torch.int32, (n,), gpu)
     _launch(
         gpu, "dspark_fork_pages",
         table.data_ptr(), held.data_ptr(), lens.data_ptr(), R, width, int(page_size),
@@ -991,7 +996,6 @@ def dspark_copy_pages(k_cache, v_cache, src, dst, slots=None):
     and values, in the caches of all layers or of one; entries outside the pool copy
     nothing."""
     gpu, pool = _layered(k_cache, v_cache)
-    _need(src, "src", torch.int32, None, gpu)
     n = src.numel()
     _need(src, "src", torch.int32, (n,), gpu)
     _need(dst, "dst", torch.int32, (n,), gpu)
