@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p,
 //
 // Trees and sinks (DSPARK_TREE=1), time spent in the parts of 128 trees of 12 to 32
 // nodes, G = 4, 175 us in all: 2.2 to 2.7 us a tile and workgroup, 7 us a unit beside
-// its tiles (of which its queries 4, its rows' results 2), 1.3 us more for a tile that
+// its tiles (of which its queries 3, its rows' results 2), 1.3 us more for a tile that
 // is masked, 12 us before the first tile, 15 us for the join. Four trees of 64 nodes
 // on 41 to 113 thousand positions in 8 bits take 467 us, 802 TFLOP/s; one tree of 60
 // nodes on 4000 32 us, a chain of waits (10 us to the first tile, six tiles, the join).
@@ -866,6 +866,30 @@ struct Tiles {
                                                               0);
         if constexpr (kk + 1 < 2 * kSub) add_values<kSub, kk + 1>(v, w, st);
     }
+#if DSPARK_TREE
+    // Whether a page of positions [k0, k1) is missing from the table: probe() asks for
+    // the first 64 of them, hole() waits.
+    struct Probe {
+        int first, last, at;  // this lane's page and its entry, the last page
+    };
+    __device__ static __forceinline__ Probe probe(const PagedCache &c, const int32_t *table, int k0,
+                                                  int k1) {
+        Probe b;
+        b.first = page_of(c, k0) + (threadIdx.x & (kWave - 1));
+        b.last = k0 < k1 ? page_of(c, k1 - 1) : -1;
+        b.at = b.first <= b.last && b.first < c.table_width ? table[b.first] : 0;
+        return b;
+    }
+    __device__ static __forceinline__ bool hole(const PagedCache &c, const int32_t *table,
+                                                const Probe &b, bool together) {
+        if (!together) return true;  // looked up key by key
+        bool any = b.last >= c.table_width || (b.first <= b.last && !named(c, b.at));
+#pragma unroll 4
+        for (int i = b.first + kWave; i <= b.last; i += kWave)
+            any |= i < c.table_width && !named(c, table[i]);
+        return __any(any);
+    }
+#else
     // Whether a page of positions [k0, k1) is missing from the table.
     __device__ static __forceinline__ bool holes(const PagedCache &c, const int32_t *table, int k0,
                                                  int k1, bool together) {
@@ -878,6 +902,7 @@ struct Tiles {
             any |= i < c.table_width && !named(c, table[i]);
         return __any(any);
     }
+#endif
 
     // kSub times 32 keys, from key 32 * sub of a staged tile on, against the wave's
     // 32 query rows.
@@ -1320,21 +1345,40 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         t.pos_max = next.q.ctx + m_last / G;
         t.active = kg < kgs && qt * 32 < rows;
 #if DSPARK_TREE
+        // queries, masks and pages are asked for together, and waited for once
+        const uint16_t *src = p.q + row * p.q_row + hq * p.q_head + (lane >> 5) * 8;
+        u32x4 x[D / 16];
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            x[ks] = u32x4{0u, 0u, 0u, 0u};
+            const bool here = !kPadded || ks * 16 + (lane >> 5) * 8 < p.D;
+            if (valid && t.active && here) x[ks] = *reinterpret_cast<const u32x4 *>(src + ks * 16);
+        }
         t.border = 0x7FFFFFFF;
         t.sinks = again.v.sinks;
+        int depth = j;
+        uint32_t bits0 = 0, bits1 = 0;
         if (again.v.masks) {
             t.border = next.q.ctx;
             t.pos_min = next.k.first;
             t.pos_max = next.k.final;
             t.mask = again.v.masks + (valid ? row : next.q.start) * again.v.words;
-            uint64_t bits = 0;
-            if (valid) {
-                t.pos = next.q.ctx + depth_of(again.v.depths, row, j);
-                if (again.v.words <= 2)
-                    bits = t.mask[0] | (again.v.words > 1 ? (uint64_t)t.mask[1] << 32 : 0u);
-            }
-            s.bits[tid] = bits;  // this lane's alone
+            if (valid) depth = again.v.depths[row];
+            if (valid && again.v.words <= 2) bits0 = t.mask[0];
+            if (valid && again.v.words == 2) bits1 = t.mask[1];
         }
+        const int i0 = next.k.tiles - next.left, sink = next.k.sink;
+        const int s0 = i0 * T::kKeys, s1 = (i0 + n < sink ? i0 + n : sink) * T::kKeys;
+        const int w0 = i0 > sink ? i0 : sink;
+        const int k0 = next.k.at(w0) * T::kKeys, k1 = next.k.at(i0 + n) * T::kKeys;
+        const auto in_sinks = T::probe(p.c, t.table, s0, s1 < t.hi ? s1 : t.hi);
+        // the window's first tile may hold some of the sinks
+        const auto in_window = T::probe(p.c, t.table, k0 > t.lo || k0 < t.sinks ? k0 : t.lo,
+                                        i0 + n > sink ? (k1 < t.hi ? k1 : t.hi) : 0);
+        t.pos += (depth < 0 ? 0 : depth > j ? j : depth) - j;
+        s.bits[tid] = bits0 | (uint64_t)bits1 << 32;  // this lane's alone
+        t.hole = T::hole(p.c, t.table, in_sinks, tp.together) ||
+                 T::hole(p.c, t.table, in_window, tp.together);
 #endif
         // a negative scale turns the queries' signs, none at all their values to 0
         const float scale = p.scale * p.c.k_scale;
@@ -1347,6 +1391,7 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
         for (int d = 0; d < D / 32; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) st.o[d][r] = 0.f;
+#if !DSPARK_TREE
         const uint16_t *src = p.q + row * p.q_row + hq * p.q_head + (lane >> 5) * 8;
         u32x4 x[D / 16];
 #pragma unroll
@@ -1355,17 +1400,8 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
             const bool here = !kPadded || ks * 16 + (lane >> 5) * 8 < p.D;
             if (valid && t.active && here) x[ks] = *reinterpret_cast<const u32x4 *>(src + ks * 16);
         }
-#if DSPARK_TREE
-        const int i0 = next.k.tiles - next.left, sink = next.k.sink;
-        const int s0 = i0 * T::kKeys, s1 = (i0 + n < sink ? i0 + n : sink) * T::kKeys;
-        const int w0 = i0 > sink ? i0 : sink;
-        const int k0 = next.k.at(w0) * T::kKeys, k1 = next.k.at(i0 + n) * T::kKeys;
-        const int end = s1 < t.hi ? s1 : t.hi;
-        t.hole = s0 < end && T::holes(p.c, t.table, s0, end, tp.together);
-        if (i0 + n > sink)  // the window's first tile may hold some of the sinks
-            t.hole |= T::holes(p.c, t.table, k0 > t.lo || k0 < t.sinks ? k0 : t.lo,
-                               k1 < t.hi ? k1 : t.hi, tp.together);
-#else
+#endif
+#if !DSPARK_TREE
         const int k0 = next.tile * T::kKeys, k1 = (next.tile + n) * T::kKeys;
         t.hole = T::holes(p.c, t.table, k0 > t.lo ? k0 : t.lo, k1 < t.hi ? k1 : t.hi, tp.together);
 #endif
