@@ -11,6 +11,7 @@ built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional
 
@@ -130,14 +131,22 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _launch(gpu: int, name: str, *args) -> None:
-    """Calls an entry point on GPU `gpu`, which need not be the current one."""
+@functools.lru_cache(maxsize=None)
+def _gpus() -> int:
+    """How many there are, fixed once a process has used one."""
+    return torch.cuda.device_count()
+
+
+def _launch(gpu: int, name: str, args) -> None:
+    """Calls an entry point on GPU `gpu`, which need not be the current one. args end
+    with the stream: passed on as they are, and the GPUs counted once, a call takes
+    as long as one without this did."""
     fn = getattr(lib(), name)
-    if torch.cuda.device_count() > 1:
+    if gpu or _gpus() > 1:
         with torch.cuda.device(gpu):
-            status = fn(*args, _raw_stream(gpu))
+            status = fn(*args)
     else:
-        status = fn(*args, _raw_stream(gpu))
+        status = fn(*args)
     if status:
         _ok(name, status)
 
@@ -163,7 +172,8 @@ def dspark_workspace_bytes(B: int, gamma: int, V: int) -> int:
 
 def dspark_workspace_init(ws: torch.Tensor) -> None:
     _need(ws, "ws", torch.uint8)
-    _launch(ws.get_device(), "dspark_workspace_init", ws.data_ptr(), ws.numel())
+    gpu = ws.get_device()
+    _launch(gpu, "dspark_workspace_init", (ws.data_ptr(), ws.numel(), _raw_stream(gpu)))
 
 
 class _Kept:
@@ -655,13 +665,13 @@ def dspark_append_kv(q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cac
     heads side by side), cos and sin [positions, rot / 2] fp32, ctx_lens [B]
     tokens cached before the call, block_table [B, width] int32, k_cache and
     v_cache [pages, Hkv, page_size, D] bf16 or float8_e4m3fn."""
-    return _append("dspark_append_kv", (), q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table,
+    return _append("dspark_append_kv", None, q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table,
                    k_cache, v_cache, interleaved, k_scale, v_scale, out)
 
 
 def _append(name, depths, q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, k_cache, v_cache,
             interleaved, k_scale, v_scale, out):
-    """dspark_append_kv, or with (depths,) dspark_append_tree_kv."""
+    """dspark_append_kv, or with depths dspark_append_tree_kv."""
     gpu, B, kind, (pages, Hkv, page, D), (ps, hs, ss, _) = _paged(
         k_cache, v_cache, cu_seqlens, ctx_lens, block_table)
     rows, Hq = q.shape[0], q.shape[1]
@@ -675,19 +685,20 @@ def _append(name, depths, q, k, v, cos, sin, cu_seqlens, ctx_lens, block_table, 
     _need(sin, "sin", torch.float32, angles, gpu)
     if len(angles) != 2:
         raise ValueError("cos must have shape (positions, rotated pairs)")
-    for t in depths:
-        _need(t, "depths", torch.int32, (rows,), gpu)
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
-    _launch(
-        gpu, name,
+    else:
+        _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
+    args = [
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], ks[0], vs[0], cos.data_ptr(),
-        sin.data_ptr(), angles[0], angles[1], 1 if interleaved else 0,
-        *[t.data_ptr() for t in depths], cu_seqlens.data_ptr(),
+        sin.data_ptr(), angles[0], angles[1], 1 if interleaved else 0, cu_seqlens.data_ptr(),
         ctx_lens.data_ptr(), B, rows, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), kind,
         pages, page, ps, hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
-        out.data_ptr())
+        out.data_ptr(), _raw_stream(gpu)]
+    if name == "dspark_append_tree_kv":
+        _need(depths, "depths", torch.int32, (rows,), gpu)
+        args.insert(11, depths.data_ptr())  # after `interleaved`
+    _launch(gpu, name, args)
     return out
 
 
@@ -734,7 +745,7 @@ def _attend(name, tree, q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, 
     else:
         _need(out, "out", torch.bfloat16, (rows, Hq, D), gpu)
     max_rows = min(int(max_rows), rows)
-    view = ()
+    view = None
     if tree is not None:
         depths, masks, sinks = tree
         if (depths is None) != (masks is None):
@@ -751,12 +762,15 @@ def _attend(name, tree, q, k_cache, v_cache, cu_seqlens, ctx_lens, block_table, 
         ws = attention_workspace(B, max_rows, Hq, Hkv, D, q.device)
     else:
         _need(ws, "ws", torch.uint8, None, gpu)
-    _launch(
-        gpu, name,
+    args = [
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), kind, pages, page, ps,
         hs, ss, k_scale, v_scale, block_table.data_ptr(), block_table.shape[1],
         cu_seqlens.data_ptr(), ctx_lens.data_ptr(), B, rows, max_rows, Hq, Hkv, D, int(window),
-        *view, D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.numel())
+        D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
+        _raw_stream(gpu)]
+    if view is not None:
+        args[24:24] = view  # after the window
+    _launch(gpu, name, args)
     return out
 
 
@@ -836,11 +850,10 @@ def dspark_tree_masks(parents, cu_seqlens, max_rows, ctx_lens=None, window=0, si
         _need(masks, "masks", torch.int32, None, gpu)
         if masks.dim() != 2 or masks.shape[0] != rows:
             raise ValueError(f"masks must have shape ({rows}, words)")
-    _launch(
-        gpu, "dspark_tree_masks",
+    _launch(gpu, "dspark_tree_masks", (
         parents.data_ptr(), cu_seqlens.data_ptr(), None if ctx_lens is None else ctx_lens.data_ptr(),
         B, rows, int(max_rows), int(window), int(sinks), masks.shape[1], depths.data_ptr(),
-        masks.data_ptr())
+        masks.data_ptr(), _raw_stream(gpu)))
     return depths, masks
 
 
@@ -849,7 +862,7 @@ def dspark_append_tree_kv(q, k, v, cos, sin, depths, cu_seqlens, ctx_lens, block
     """dspark_append_kv for the nodes of trees: a row is rotated by the position
     ctx_lens[b] + depths[row] (dspark_tree_masks) and keeps the slot that it has in a
     chain. Returns the rotated queries."""
-    return _append("dspark_append_tree_kv", (depths,), q, k, v, cos, sin, cu_seqlens, ctx_lens,
+    return _append("dspark_append_tree_kv", depths, q, k, v, cos, sin, cu_seqlens, ctx_lens,
                    block_table, k_cache, v_cache, interleaved, k_scale, v_scale, out)
 
 
@@ -887,11 +900,10 @@ def dspark_tree_accept(packed_choice, packed_tokens, parents, cu_seqlens, max_ro
         _need(acc, "accepted", torch.int32, (B,), gpu)
         _need(bonus, "bonus", torch.int32, (B,), gpu)
         _need(path, "path", torch.int32, (B, width), gpu)
-    _launch(
-        gpu, "dspark_tree_accept",
+    _launch(gpu, "dspark_tree_accept", (
         packed_choice.data_ptr(), packed_tokens.data_ptr(), parents.data_ptr(),
         cu_seqlens.data_ptr(), B, rows, int(max_rows), int(width), acc.data_ptr(),
-        bonus.data_ptr(), path.data_ptr())
+        bonus.data_ptr(), path.data_ptr(), _raw_stream(gpu)))
     return acc, bonus, path
 
 
@@ -931,8 +943,9 @@ def dspark_move_kv(k_cache, v_cache, path, accepted, ctx_lens, block_table):
     _need(block_table, "block_table", torch.int32, None, gpu)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, pages of a request)")
-    _launch(gpu, "dspark_move_kv", *pool, path.data_ptr(), accepted.data_ptr(), width,
-            ctx_lens.data_ptr(), block_table.data_ptr(), block_table.shape[1], B)
+    _launch(gpu, "dspark_move_kv", (
+        *pool, path.data_ptr(), accepted.data_ptr(), width, ctx_lens.data_ptr(),
+        block_table.data_ptr(), block_table.shape[1], B, _raw_stream(gpu)))
 
 
 def page_pool(pages: int, rows: int, width: int, device):
@@ -963,8 +976,9 @@ def dspark_resize_pages(table, held, refs, lens, page_size, granted=None):
         granted = torch.empty_like(held)
     else:
         _need(granted, "granted", torch.int32, (R,), gpu)
-    _launch(gpu, "dspark_resize_pages", table.data_ptr(), held.data_ptr(), lens.data_ptr(), R,
-            width, int(page_size), refs.data_ptr(), refs.numel(), granted.data_ptr())
+    _launch(gpu, "dspark_resize_pages", (
+        table.data_ptr(), held.data_ptr(), lens.data_ptr(), R, width, int(page_size),
+        refs.data_ptr(), refs.numel(), granted.data_ptr(), _raw_stream(gpu)))
     return granted
 
 
@@ -983,11 +997,10 @@ def dspark_fork_pages(table, held, refs, src, dst, lens, page_size, out=None):
     else:
         for t, name in zip(out, ("copy_src", "copy_dst", "copy_slots", "granted")):
             _need(t, name, torch.int32, (n,), gpu)
-    _launch(
-        gpu, "dspark_fork_pages",
+    _launch(gpu, "dspark_fork_pages", (
         table.data_ptr(), held.data_ptr(), lens.data_ptr(), R, width, int(page_size),
         refs.data_ptr(), refs.numel(), src.data_ptr(), dst.data_ptr(), n,
-        *[t.data_ptr() for t in out])
+        *[t.data_ptr() for t in out], _raw_stream(gpu)))
     return out
 
 
@@ -1001,8 +1014,9 @@ def dspark_copy_pages(k_cache, v_cache, src, dst, slots=None):
     _need(dst, "dst", torch.int32, (n,), gpu)
     if slots is not None:
         _need(slots, "slots", torch.int32, (n,), gpu)
-    _launch(gpu, "dspark_copy_pages", *pool, src.data_ptr(), dst.data_ptr(),
-            None if slots is None else slots.data_ptr(), n)
+    _launch(gpu, "dspark_copy_pages", (
+        *pool, src.data_ptr(), dst.data_ptr(), None if slots is None else slots.data_ptr(), n,
+        _raw_stream(gpu)))
 
 
 __all__ = ["DsparkError", "lib", "LIB_PATH", "dspark_status_string", "dspark_confidence", "dspark_schedule",
