@@ -25,7 +25,8 @@ def handed_out_whole(c, window=0, sinks=0):
     times the even division. A unit has a place for each of its tiles and four more."""
     Hkv, item = c["kc"].shape[1], c["kc"].element_size()
     keys = 16384 // ((64 if c["D"] <= 64 else 128) * item)  # positions of a tile
-    wgs, places = 2 * CUS, []
+    wide = c["max_rows"] * c["Hq"] // Hkv > 128  # blocks of 256 rows, one workgroup a CU
+    wgs, places = CUS if wide else 2 * CUS, []
     for b, ctx in enumerate(c["ctx"]):
         n = c["cu"][b + 1] - c["cu"][b]
         first = max(0, ctx + 1 - window) // keys if window else 0
@@ -92,6 +93,20 @@ def test_units_without_a_window(B, whole):
     c = tree(make(rows, [650 + b % 40 for b in range(B)], 16, 8, 128, 16, seed=B), B)
     check(c, whole)
     check(without(c), whole)
+
+
+@pytest.mark.parametrize("B,whole", [(32, True), (33, False), (64, True)])
+@pytest.mark.parametrize("D,cache,window,sinks,ctx", [
+    (64, "bf16", 400, 4, 900), (128, "e4m3", 300, 20, 900), (128, "bf16", 0, 0, 400)])
+def test_units_of_more_than_128_rows(B, whole, D, cache, window, sinks, ctx):
+    """One and two a workgroup in blocks of 256 rows; eight too many for one."""
+    rng = random.Random(B + D)
+    kw = dict(window=window, sinks=sinks, **SCALES[cache])
+    rows, lens = [rng.randint(8, 12) for _ in range(B)], [ctx + b % 7 for b in range(B)]
+    rows[0] = 33  # of one tree alone, so that the definition is soon computed
+    c = tree(make(rows, lens, 32, 8, D, 16, cache, seed=B), B, window, sinks)
+    check(c, whole, **kw)
+    check(without(c), whole, **kw)
 
 
 @pytest.mark.parametrize("short,whole", [(0, True), (47, True), (48, False), (60, False)])
