@@ -71,7 +71,10 @@ __device__ __forceinline__ float load1(const void *pool, int64_t at) {
 // time, a lane per key for the scores and a lane per output element for the
 // weighted values. Bound by its latency: 32 requests of mixed traffic at D = 96 took
 // 2127 us here and take 66 us in the tiles below, so only heads over 128 and pools
-// that 16-byte loads do not fit come here.
+// that 16-byte loads do not fit come here. Keys and values are read again for every row
+// and query head: one tree of 60 nodes on 4000 positions with 8 + 2 heads of 256 takes
+// 4.4 ms, 32 trees of 12 to 32 nodes 3.7 ms; 45 us the latter with 16 + 4 heads of 128,
+// as many bytes, in the tiles.
 template <bool kE4m3>
 __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p, TreeView v) {
     __shared__ float q_s[kMaxHeadDim];
@@ -190,12 +193,17 @@ __global__ __launch_bounds__(kRowThreads) void attend_row_kernel(AttendParams p,
 // registers, whose reloads wait behind the loads into LDS. Figures of one card;
 // others took 1 to 5 % more or less.
 //
-// Trees and sinks (DSPARK_TREE=1), time spent in the parts of 128 trees of 12 to 32
-// nodes, G = 4, 175 us in all: 2.2 to 2.7 us a tile and workgroup, 7 us a unit beside
-// its tiles (of which its queries 3, its rows' results 2), 1.3 us more for a tile that
-// is masked, 12 us before the first tile, 15 us for the join. Four trees of 64 nodes
-// on 41 to 113 thousand positions in 8 bits take 467 us, 802 TFLOP/s; one tree of 60
-// nodes on 4000 32 us, a chain of waits (10 us to the first tile, six tiles, the join).
+// Trees and sinks (DSPARK_TREE=1): 128 trees of 12 to 32 nodes, G = 4, take 178 us, 15
+// of them in the join. Where each workgroup has one whole unit, of 64 trees of 12 (24)
+// nodes in windows of 256 to 2048, a tile takes 3.3 (3.9) us with all of them loading,
+// 5.1 (4.3) TB/s; a second unit takes 5 to 9 us beside its tiles. Four trees of 64 nodes
+// on 41 to 113 thousand positions in 8 bits take 449 us, 834 TFLOP/s. One tree of 60
+// nodes on 4000 takes 31 us, a chain of waits: the tiles' kernel 16 us where units have
+// one tile, 2.1 for each further one up to the five that a workgroup takes at least, 28
+// on 4000, then 4 for the join. Trees of more than 64 nodes read their masks' words from
+// memory, behind the tiles on their way: 64 of 100 to 256 nodes on 128 to 4096 positions
+// take 529 us, 3.0 times what their operations need; 64 of 32 to 64 nodes take 172, 2.3
+// times what their bytes need.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds 16 of a query's 32
 // scores of one MFMA (the other 16 sit in lane ^ 32), so the softmax needs one
@@ -709,8 +717,8 @@ struct Tiles {
         return n >= 32 ? 0xFFFFFFFFu : (1u << (n < 0 ? 0 : n)) - 1u;
     }
     // The positions of 32 from k0 on that this lane's query row sees, if they have pages,
-    // as bits. The bits of the row's mask are kept in LDS: a load from memory would wait
-    // for the tiles on their way.
+    // as bits. Up to 64 bits of the row's mask are kept in LDS: a load from memory, which
+    // more of them take, waits for the tiles on their way.
     __device__ static __forceinline__ uint32_t seen(const AttendParams &p, const Lds &s,
                                                     const Task &t, int k0) {
         const int64_t past = (int64_t)k0 - t.border;  // the border is past all keys of a chain
@@ -1100,9 +1108,13 @@ __global__ __launch_bounds__(kWide ? 512 : 256, 2) void attend_tile_kernel(TileP
     const uint64_t total = s.before[p.B];
 #if DSPARK_TREE
     // Where all requests have one block and about as many tiles (decoding and trees in
-    // a window), every workgroup gets as many whole units as another and none is cut:
-    // 64 trees in a window of 1024 take 62 us, 77 cut. Allowed to take 30 % longer than
-    // the even division by tiles, which is less than what its cuts cost.
+    // a window), every workgroup gets as many whole units as another and none is cut,
+    // if that takes up to 30 % longer than the even division by tiles. Short units gain
+    // by it: 512 of single tokens in windows of 512 and 1024 take 43 and 69 us, cut 48
+    // and 74, of trees of 12 to 24 nodes 57 and 81, cut 67 and 91; on 3000 to 4000
+    // positions 190 and 202, cut 193 and 219. For long ones it matters little: on 12 to
+    // 16 thousand positions, the longest 1.14 times the mean, trees take 679 us, cut 696,
+    // and single tokens 636, cut 620.
     bool whole_units = false;
     if ((int64_t)p.max_rows * G <= block_rows) {
         uint32_t most = 0;

@@ -461,9 +461,10 @@ static dspark_status append_rows(
     const dspark_bf16 *q, const dspark_bf16 *k, const dspark_bf16 *v, long long q_stride,
     long long k_stride, long long v_stride, const float *cos, const float *sin, int positions,
     int half, int interleaved, const int32_t *depths, const int32_t *cu_seqlens,
-    const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv, int D, void *k_cache, void *v_cache, int cache_type, int pages, int page_size,
-    long long page_stride, long long head_stride, long long slot_stride, float k_scale,
-    float v_scale, const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
+    const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv, int D, void *k_cache,
+    void *v_cache, int cache_type, int pages, int page_size, long long page_stride,
+    long long head_stride, long long slot_stride, float k_scale, float v_scale,
+    const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
     if (!q || !k || !v || !cu_seqlens || !ctx_lens || !k_cache || !v_cache || !block_table || !q_out)
         return DSPARK_ERR_NULL;
     if (half > 0 && (!cos || !sin)) return DSPARK_ERR_NULL;
@@ -520,9 +521,10 @@ DSPARK_API dspark_status dspark_append_tree_kv(
     const dspark_bf16 *q, const dspark_bf16 *k, const dspark_bf16 *v, long long q_stride,
     long long k_stride, long long v_stride, const float *cos, const float *sin, int positions,
     int half, int interleaved, const int32_t *depths, const int32_t *cu_seqlens,
-    const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv, int D, void *k_cache, void *v_cache, int cache_type, int pages, int page_size,
-    long long page_stride, long long head_stride, long long slot_stride, float k_scale,
-    float v_scale, const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
+    const int32_t *ctx_lens, int B, int rows, int Hq, int Hkv, int D, void *k_cache,
+    void *v_cache, int cache_type, int pages, int page_size, long long page_stride,
+    long long head_stride, long long slot_stride, float k_scale, float v_scale,
+    const int32_t *block_table, int table_width, dspark_bf16 *q_out, void *stream) {
     if (!depths) return DSPARK_ERR_NULL;
     return append_rows(q, k, v, q_stride, k_stride, v_stride, cos, sin, positions, half,
                        interleaved, depths, cu_seqlens, ctx_lens, B, rows, Hq, Hkv, D, k_cache,

@@ -125,9 +125,12 @@ __device__ __forceinline__ int owner(const int *before, int x) {
 // One workgroup, 1024 rows at a time: first every row's pages past its length are
 // released, then the rows that need more take theirs. Both work on the entries of
 // all rows laid end to end, so one long row costs no more than many short ones. A
-// chain of dependent reads: 2.3 to 4.6 us for up to a thousand rows that give or take
-// a page; 12000 releases 19 us, by the rate of one compute unit's atomics (more
-// workgroups would need a second launch before pages are taken).
+// chain of dependent reads: 2.4 us for 8 to 1000 rows that keep what they hold, 3.8 to
+// 7.5 where each gives a page back and 6.2 to 8.3 where each takes one and free pages are
+// among the first 16384; 12000 releases 19 us, by the rate of one compute unit's atomics
+// (more workgroups would need a second launch before pages are taken). The search for
+// free pages begins at page 0 in every call that takes any, 4 us for every 16384 pages
+// that it passes: 30 us in all behind 100 000 taken pages, 250 behind a million.
 __global__ __launch_bounds__(kPoolThreads) void resize_pages_kernel(PoolParams p) {
     __shared__ int before_s[kPoolThreads], held_s[kPoolThreads], lds[kPoolWords];
     auto rows_from = [&](int b0, int &held, int &want) {
@@ -238,8 +241,10 @@ __device__ __forceinline__ int fork_row(const PoolParams &p, int i, int tid, int
 
 // One workgroup: which forks are granted, and a fresh page for each that ends
 // inside a page. kAll: and the forks themselves, a wave each. A chain of six dependent
-// reads: three forks 6.4 us, 224 on cold caches 17 us, of which the comparison of
-// every target with all rows named is 2 to 3.
+// reads, 6.6 us for three forks and 7.5 for 17 (3 more on cold caches), and the
+// comparison of every target with all rows named, 0.05 us a fork: 64 forks take 9.5 us,
+// 224 17, 512 33 and 1024 77, and every 1024 are compared with all. Free pages are
+// searched for as by resize_pages_kernel.
 template <bool kAll>
 __global__ __launch_bounds__(kPoolThreads) void fork_plan_kernel(PoolParams p) {
     typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -322,7 +327,7 @@ __global__ __launch_bounds__(kPoolThreads) void fork_apply_kernel(PoolParams p) 
 
 // Copies `slots` slots of a page in every layer, keys and values: an item is one
 // T of one (head, slot), eight of them on their way a thread. Bound by bytes: 224 pages
-// of 8 layers, 451 MB read and written, take 92 us, 4.9 TB/s.
+// of 8 layers, 451 MB read and written, take 91 us, 5.0 TB/s.
 template <typename T>
 __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(PageMoveParams p) {
     const int src = p.src[blockIdx.x], dst = p.dst[blockIdx.x];
@@ -361,7 +366,7 @@ __global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(PageMoveParams
 // path[i]. A thread owns the same T of every position and layer, and path[i] >= i
 // rises, so eight positions may be read before any of them is written, and no
 // later one is written over before it is read. 256 requests in 16 layers, 34 MB read and
-// written, take 12 us: four dependent reads (count, path, table, keys) and the launch.
+// written, take 11 us: four dependent reads (count, path, table, keys) and the launch.
 template <typename T>
 __global__ __launch_bounds__(kMoveThreads) void move_kv_kernel(PageMoveParams p) {
     __shared__ int64_t from_s[kMoveThreads], to_s[kMoveThreads];
@@ -418,7 +423,7 @@ hipError_t launch_resize_pages(const PoolParams &p, hipStream_t s) {
 }
 
 hipError_t launch_fork_pages(const PoolParams &p, hipStream_t s) {
-    // One launch for as many forks as waves, of short rows: three forks take 6.4 us so,
+    // One launch for as many forks as waves, of short rows: three forks take 6.6 us so,
     // 9.4 in two launches, which longer rows need to be spread over the device.
     if (p.n <= kPoolWaves && p.width <= 4 * kWave) {
         hipLaunchKernelGGL((fork_plan_kernel<true>), dim3(1), dim3(kPoolThreads), 0, s, p);

@@ -28,10 +28,13 @@ __device__ __forceinline__ int parent_of(int parent, int j) {
 // node to its root for one word of that node's mask. An ancestor `step` levels up
 // is in the window when step < window, and among the first positions when
 // ctx + depth - step < sinks. The depth is known at the end of the walk, so those
-// few rows that need it walk twice. Bound by its launch and three dependent reads: one
-// tree of 32 nodes takes 2.6 us, 192 of up to 64 nodes 4.6. Walks beside each other
-// take as many steps as a tree is deep; filling the masks node by node would take as
-// many as it has nodes.
+// few rows that need it walk twice. Up to 64 nodes it is bound by its launch and three
+// dependent reads: one tree of 32 nodes takes 2.7 us, 192 of up to 64 nodes 4.4. Walks
+// beside each other take as many steps as a tree is deep; filling the masks node by node
+// would take as many as it has nodes. But each word of a node is a walk of its own, and
+// 256 threads share nodes x words of them: one tree of 256 nodes, 10 deep, takes 11 us
+// (64 such trees 12), one of 1024 nodes 123, a chain of 256 nodes 99 us and one of 1024
+// 5.5 ms (11 with sinks past its window); one walk a node would be a 32nd of these steps.
 __global__ __launch_bounds__(kMaskThreads) void tree_masks_kernel(TreeMaskParams p) {
     __shared__ int parent_s[DSPARK_MAX_TREE];
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {

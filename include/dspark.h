@@ -505,8 +505,12 @@ dspark_status dspark_sample_accept(const dspark_bf16 *logits, const int32_t *pac
  * and dspark_tree_attention, then the target's choices (packed_argmax of
  * dspark_accept or packed_sample of dspark_sample_accept), dspark_tree_accept, and
  * dspark_move_kv, which brings the accepted nodes' keys and values together.
+ * A choice is its row's own. A tree of more rows than a block of those calls holds
+ * (gamma + 1, at most DSPARK_MAX_GAMMA + 1) is given to them as several requests, by a
+ * cu_seqlens that cuts its rows (with its filters for each of them); their accepted
+ * and bonus are not used then.
  */
-#define DSPARK_MAX_TREE 1024        /* nodes of a request's tree */
+#define DSPARK_MAX_TREE 1024 /* nodes of a request's tree */
 #define DSPARK_MAX_TABLE_ROWS (1 << 20)
 #define DSPARK_MAX_FORKS 16384
 
@@ -564,8 +568,8 @@ dspark_status dspark_append_tree_kv(const dspark_bf16 *q, const dspark_bf16 *k,
  * t < sinks.
  * Positions whose page the table does not name are not seen. depths [rows], masks
  * [rows, mask_words] int32: both or neither (DSPARK_ERR_NULL); DSPARK_ERR_SHAPE for
- * mask_words * 32 below the smaller of max_rows and rows; DSPARK_ERR_ARG for
- * negative sinks. Everything else, the weights' rounding, rows that see nothing,
+ * mask_words * 32 below the smaller of max_rows and rows or above DSPARK_MAX_ROWS;
+ * DSPARK_ERR_ARG for negative sinks. Everything else, the weights' rounding, rows that see nothing,
  * values that are not finite, the alignment and the workspace, is as for
  * dspark_verify_attention, whose workspace serves both.
  */
@@ -581,14 +585,16 @@ dspark_status dspark_tree_attention(const dspark_bf16 *q, long long q_row, long 
                                     size_t ws_bytes, void *stream);
 
 /*
- * The longest way down a tree that the target agrees with. From row 0 of request
+ * The way down a tree that the target agrees with. From row 0 of request
  * b on, the next row is the lowest one that has the current row for its parent and
  * the target's choice at the current row for its token:
  *   path[b, 0] = 0, path[b, i+1] = min{c : parents[c] = path[b, i],
  *                                      packed_tokens[c] = packed_choice[path[b, i]]}
  *   accepted[b] = the number of steps, at most width - 1
  *   bonus[b]    = packed_choice[path[b, accepted[b]]]
- * (places among the request's rows). Entries of path past accepted[b] are -1; a
+ * (places among the request's rows). Where siblings share a token the lowest one is
+ * taken, also if another one leads further down: a drafter gives siblings tokens of
+ * their own. Entries of path past accepted[b] are -1; a
  * request without rows gets accepted 0, bonus -1 and a path of -1. On a chain this
  * is dspark_accept's result.
  * packed_choice, packed_tokens, parents [rows], cu_seqlens [B+1] int32; rows of a
@@ -639,7 +645,9 @@ dspark_status dspark_move_kv(void *k_cache, void *v_cache, int cache_type, int l
  * needs more than `width` pages is left as it is. granted[b] is 1 where row b holds
  * what its length needs. Negative lengths count as 0.
  *   Called with ctx_lens plus a step's rows before the step, and with 0 for a
- * request that ends, it is all the page keeping of a serving loop. A page that
+ * request that ends, it is all the page keeping of a serving loop. A call that takes
+ * pages searches refs from page 0 on: its time grows with the pages that are taken
+ * below (by 23 us for 100 000). A page that
  * several rows share is for reading: a row cut back into one needs dspark_fork_pages
  * before more is appended to it.
  * table, held, refs int32 in and out; lens [R] int32; granted [R] int32 output.
